@@ -252,9 +252,10 @@ int nvfp4_linear_swiglu(const void *X, int64_t M, int64_t K,
                         unsigned flags, void *ws, size_t ws_bytes, void *stream);
 
 /* Synchronizes `stream`, then returns and clears the device status word of
- * the current device: NVFP4_OK, NVFP4_ERR_TIMEOUT or NVFP4_ERR_NONFINITE
- * (timeout wins when both are latched), or NVFP4_ERR_CUDA if the sync
- * failed. */
+ * the current device: NVFP4_OK, NVFP4_ERR_TIMEOUT, NVFP4_ERR_NONFINITE or
+ * NVFP4_ERR_INVALID_ARG (a kernel met a length, offset or page index out of
+ * range); when several are latched, the first of these wins.  NVFP4_ERR_CUDA
+ * if the sync failed. */
 int nvfp4_get_status(void *stream);
 
 /* Static, NUL-terminated description of a status code. */
@@ -332,6 +333,140 @@ int nvfp4_fp8_kv_calibrate(const void *X, int64_t rows, int64_t cols, int64_t ld
  * finite number nothing is written and NVFP4_ERR_NONFINITE is latched. */
 int nvfp4_fp8_kv_quantize(const void *X, int64_t rows, int64_t cols, int64_t ldx, const float *scale, uint8_t *out,
                           int64_t ldo, void *stream);
+
+/* ------------------------------------- attention over the paged FP8 KV cache
+ *
+ * What an attention layer runs between its fused q/k/v projection and its
+ * output projection, in serving: the norm and rotation of the query and key
+ * heads, the append of keys and values to the paged E4M3 cache (the codes and
+ * scales of nvfp4_fp8_kv_quantize), and the attention of the new tokens over
+ * that cache.  The pages this library follows take the attention layers as
+ * given and only report that their KV cache ships calibrated FP8 scales
+ * (freegardner.com, "The Calibrated Cache That Ships for Free"); the layer
+ * around the cache is the usual one.
+ *
+ * Every struct below is a HOST struct, read before the call returns; the
+ * pointers inside are DEVICE pointers. */
+
+/* Head rows of a token-major bf16 tensor: row (t, h) holds head_dim
+ * contiguous elements at data + t * token_stride + h * head_stride (strides
+ * in elements, multiples of 8; data 16-byte aligned).  A view of a wider
+ * projection, e.g. the queries of an interleaved query/gate projection, is
+ * described without a copy. */
+typedef struct {
+    void *data;
+    int64_t token_stride;
+    int64_t head_stride;
+    int64_t heads;
+} nvfp4_heads;
+
+/* Pages of one layer's cache: E4M3 codes, K and V row (page, r, h) at
+ * k_pages + page * page_stride + r * token_stride + h * head_stride (bytes;
+ * multiples of 16, each a multiple of the next smaller one, bases 16-byte
+ * aligned), head_dim contiguous bytes.  page_size is a power of two from 16
+ * to 256, head_dim 128 or 256.  k_scale and v_scale: device fp32, the
+ * calibrated decode multipliers of the two caches. */
+typedef struct {
+    void *k_pages;
+    void *v_pages;
+    const float *k_scale;
+    const float *v_scale;
+    int64_t k_page_stride, k_token_stride, k_head_stride;
+    int64_t v_page_stride, v_token_stride, v_head_stride;
+    int64_t num_pages;
+    int32_t page_size;
+    int32_t kv_heads;
+    int32_t head_dim;
+} nvfp4_kv_pages;
+
+/* The batch of a step (device int32 arrays, read by the kernels, so a
+ * captured graph may be replayed with new contents): sequence b owns the
+ * token rows [cu_tokens[b], cu_tokens[b+1]) (cu_tokens[0] = 0) and has
+ * seq_lens[b] cached positions, its new tokens included: new token j sits at
+ * position seq_lens[b] - new_b + j.  Position p lives in page
+ * page_table[b * table_stride + p / page_size], row p % page_size.  Entries
+ * beyond a sequence's last page are not read.  Token rows at or behind
+ * cu_tokens[num_seqs] belong to no sequence and are left alone.  A token
+ * whose position is negative (seq_lens[b] < new_b) is not cached and sees no
+ * key.  Lengths or offsets out of range, and table entries outside [0,
+ * num_pages), latch NVFP4_ERR_INVALID_ARG (nvfp4_get_status); memory outside
+ * the pages is never touched, the affected sequences' outputs are
+ * unspecified. */
+typedef struct {
+    const int32_t *page_table;
+    const int32_t *cu_tokens;
+    const int32_t *seq_lens;
+    int64_t table_stride;
+    int32_t num_seqs;
+    int32_t max_pages;
+} nvfp4_kv_batch;
+
+/* Head norm and rotation: y = x * rsqrt(mean(x^2) + eps) * w over a head's
+ * elements (bf16 weights [head_dim]; a null weight: no norm, y = x;
+ * NVFP4_NORM_PLUS_ONE: 1 + w in place of w), then for i < rotary_dim / 2 the
+ * pair (y[i], y[i + rotary_dim / 2]) is turned by the angle position *
+ * inv_freq[i] (device fp32; the product and its reduction by multiples of 2
+ * pi in fp64).  rotary_dim is a multiple of 16, at most head_dim; 0: no
+ * rotation, inv_freq may be null.  fp32 throughout, one rounding at the end. */
+typedef struct {
+    const void *q_weight;
+    const void *k_weight;
+    const float *inv_freq;
+    int32_t rotary_dim;
+    float eps;
+    unsigned flags;
+} nvfp4_norm_rope;
+
+#define NVFP4_NORM_PLUS_ONE 8u /* nvfp4_norm_rope.flags: norm weights are stored as w - 1 */
+
+/* Norm and rotation of all query and key heads in one pass: q_out and k_out
+ * (bf16, rounded to nearest even) from q and k, tokens rows each.
+ * positions: device int32 [tokens].  k (and k_out) may be null.  An output
+ * may be its input (same data and strides); other overlaps are not allowed. */
+int nvfp4_qk_norm_rope(const nvfp4_heads *q, const nvfp4_heads *k, const nvfp4_heads *q_out, const nvfp4_heads *k_out,
+                       int64_t tokens, int64_t head_dim, const int32_t *positions, const nvfp4_norm_rope *norm_rope,
+                       void *stream);
+
+/* Appends the batch's new tokens to the cache: K rows after the norm
+ * (k_weight) and rotation of nvfp4_norm_rope, V rows as they are, each code =
+ * E4M3_RNE_satfinite(fl32(y / scale)).  positions (device int32 [tokens])
+ * gives the rotation's positions; null: the tokens' cache positions.  Pages
+ * that receive new tokens must belong to one sequence alone.  A scale that is
+ * not a positive finite number: nothing is written and NVFP4_ERR_NONFINITE is
+ * latched. */
+int nvfp4_fp8_kv_append(const nvfp4_heads *k, const nvfp4_heads *v, int64_t tokens, const nvfp4_kv_pages *cache,
+                        const nvfp4_kv_batch *batch, const int32_t *positions, const nvfp4_norm_rope *norm_rope,
+                        void *stream);
+
+typedef struct {
+    float softmax_scale; /* positive, finite */
+    unsigned flags;      /* 0 */
+} nvfp4_attention_opts;
+
+/* Workspace bytes of nvfp4_fp8_kv_attention (0 for invalid sizes). */
+size_t nvfp4_fp8_kv_attention_workspace_bytes(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t head_dim);
+
+/* Causal attention of the batch's new tokens over their sequences' pages
+ * (which already hold the new tokens).  Query head h reads key head h /
+ * (q_heads / kv_heads); the token at position p sees keys 0 .. p:
+ *   s_i = softmax_scale * k_scale * sum_d q[d] k_code[i][d],
+ *   out = v_scale * sum_i exp(s_i - max) v_code[i] / sum_i exp(s_i - max),
+ * times 1 / (1 + exp(-gate)) when gate (same shape as q) is not null, rounded
+ * to bf16.  A token that sees no key gets zeros.  Keys out of sight never
+ * influence a token, whatever bytes they hold.  out_amax, if not null,
+ * receives max|out| over the rows written (bf16 magnitude bits, the form
+ * NVFP4_AMAX_GIVEN takes).  out must not overlap q or gate.  q_heads is a
+ * multiple of kv_heads, at most 128 times it.
+ * Softmax statistics and sums are fp32; queries enter the FP8 MMA as the sum
+ * of two E4M3 terms, which hold all 8 bits of a bf16 value (values below
+ * 2^-10 of their row's largest lose low bits), probabilities as the sum of
+ * two E4M3 terms of 8 bits together.  The order of the sums depends on the
+ * lengths of the whole batch: the same call gives the same bits.
+ * ws: nvfp4_fp8_kv_attention_workspace_bytes(...) bytes, 16-byte aligned,
+ * scratch only: nothing is kept in it between calls. */
+int nvfp4_fp8_kv_attention(const nvfp4_heads *q, const nvfp4_heads *gate, const nvfp4_heads *out, int64_t tokens,
+                           const nvfp4_kv_pages *cache, const nvfp4_kv_batch *batch, const nvfp4_attention_opts *opts,
+                           uint32_t *out_amax, void *ws, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

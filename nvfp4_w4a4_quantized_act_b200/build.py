@@ -27,8 +27,14 @@ def sources() -> list[str]:
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def attention_sources() -> list[str]:
+    return sorted(glob.glob(os.path.join(CSRC, "attention", "*.cu")))
+
+
 def deps() -> list[str]:
-    return sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [os.path.join(INCLUDE, "nvfp4.h")]
+    headers = [f for d in (CSRC, os.path.join(CSRC, "attention")) for ext in ("*.cuh", "*.h")
+               for f in sorted(glob.glob(os.path.join(d, ext)))]
+    return sources() + attention_sources() + headers + [os.path.join(INCLUDE, "nvfp4.h")]
 
 
 def up_to_date() -> bool:
@@ -42,7 +48,7 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     if not force and up_to_date():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [NVCC, *NVCC_FLAGS, *(extra or []), "-o", tmp, *sources()]
+    cmd = [NVCC, *NVCC_FLAGS, *(extra or []), "-o", tmp, *sources(), *attention_sources()]
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.check_call(cmd)

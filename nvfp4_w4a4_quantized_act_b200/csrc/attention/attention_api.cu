@@ -1,0 +1,342 @@
+// attention_api.cu -- the attention layer's entry points of the C ABI: head
+// norms and rotation, the paged FP8 cache's append, attention over it.
+// Argument checks and launches; declared and documented in include/nvfp4.h.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "nvfp4.h"
+#include "head_rows_kernels.cuh"
+#include "host.h"
+#include "paged_attention_simple.cuh"
+#include "paged_batch.cuh"
+
+namespace {
+
+using nvfp4::host::launch;
+namespace attn = nvfp4::attn;
+
+inline bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+int launch_ok() { return nvfp4::host::launch_failed() ? NVFP4_ERR_CUDA : NVFP4_OK; }
+
+int check_head_dim(int64_t d) { return (d == 128 || d == 256) ? NVFP4_OK : NVFP4_ERR_UNSUPPORTED_SHAPE; }
+
+constexpr int64_t kMaxTokens = int64_t(1) << 24;
+constexpr int64_t kMaxHeads = 1024;
+
+int check_heads(const nvfp4_heads *x, int64_t tokens)
+{
+    if (x == nullptr || x->heads < 1 || (tokens > 0 && x->data == nullptr))
+        return NVFP4_ERR_INVALID_ARG;
+    if (x->heads > kMaxHeads)
+        return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned(x->data, 16) || x->token_stride % 8 != 0 || x->head_stride % 8 != 0)
+        return NVFP4_ERR_MISALIGNED;
+    return NVFP4_OK;
+}
+
+int check_tokens(int64_t tokens)
+{
+    if (tokens < 0)
+        return NVFP4_ERR_INVALID_ARG;
+    return tokens <= kMaxTokens ? NVFP4_OK : NVFP4_ERR_UNSUPPORTED_SHAPE;
+}
+
+// `weight`: the norm weight that this call reads.
+int check_norm_rope(const nvfp4_norm_rope *n, int64_t head_dim)
+{
+    if (n == nullptr || (n->flags & ~NVFP4_NORM_PLUS_ONE) != 0 || n->rotary_dim < 0 || !(n->eps >= 0.0f) ||
+        !std::isfinite(n->eps) || (n->rotary_dim > 0 && n->inv_freq == nullptr))
+        return NVFP4_ERR_INVALID_ARG;
+    if (n->rotary_dim % 16 != 0 || n->rotary_dim > head_dim)
+        return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned(n->q_weight, 16) || !aligned(n->k_weight, 16) || !aligned(n->inv_freq, 4))
+        return NVFP4_ERR_MISALIGNED;
+    return NVFP4_OK;
+}
+
+// Strides of a tensor map in the order of their size, each a multiple of the
+// one before it, as the map's definition asks.
+bool strides_nest(int64_t a, int64_t b, int64_t c)
+{
+    int64_t s[3] = {a, b, c};
+    std::sort(s, s + 3);
+    return s[0] > 0 && s[1] % s[0] == 0 && s[2] % s[1] == 0;
+}
+
+int check_pages(const nvfp4_kv_pages *c)
+{
+    if (c == nullptr || c->k_pages == nullptr || c->v_pages == nullptr || c->k_scale == nullptr ||
+        c->v_scale == nullptr || c->num_pages < 1 || c->kv_heads < 1)
+        return NVFP4_ERR_INVALID_ARG;
+    int rc = check_head_dim(c->head_dim);
+    if (rc != NVFP4_OK)
+        return rc;
+    if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)) != 0 ||
+        c->kv_heads > kMaxHeads || c->num_pages >= (int64_t(1) << 31))
+        return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    const int64_t strides[6] = {c->k_page_stride, c->k_token_stride, c->k_head_stride,
+                                c->v_page_stride, c->v_token_stride, c->v_head_stride};
+    for (int64_t s : strides) {
+        if (s < c->head_dim)
+            return NVFP4_ERR_INVALID_ARG;
+        if (s % 16 != 0)
+            return NVFP4_ERR_MISALIGNED;
+        if (s >= (int64_t(1) << 40))
+            return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    }
+    if (!strides_nest(c->k_page_stride, c->k_token_stride, c->k_head_stride) ||
+        !strides_nest(c->v_page_stride, c->v_token_stride, c->v_head_stride) || !aligned(c->k_pages, 16) ||
+        !aligned(c->v_pages, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
+        return NVFP4_ERR_MISALIGNED;
+    return NVFP4_OK;
+}
+
+int check_batch(const nvfp4_kv_batch *b, int32_t page_size)
+{
+    if (b == nullptr || b->num_seqs < 0 || b->max_pages < 0)
+        return NVFP4_ERR_INVALID_ARG;
+    if (b->num_seqs > 0 && (b->cu_tokens == nullptr || b->seq_lens == nullptr ||
+                            (b->max_pages > 0 && b->page_table == nullptr) || b->table_stride < b->max_pages))
+        return NVFP4_ERR_INVALID_ARG;
+    // positions are 32-bit
+    if (b->num_seqs > (1 << 20) || int64_t(b->max_pages) * page_size >= (int64_t(1) << 31))
+        return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned(b->cu_tokens, 4) || !aligned(b->seq_lens, 4) || !aligned(b->page_table, 4))
+        return NVFP4_ERR_MISALIGNED;
+    return NVFP4_OK;
+}
+
+attn::HeadRows rows_of(const nvfp4_heads *x)
+{
+    attn::HeadRows r;
+    r.data = x == nullptr ? nullptr : static_cast<const uint16_t *>(x->data);
+    r.token_stride = x == nullptr ? 0 : x->token_stride;
+    r.head_stride = x == nullptr ? 0 : x->head_stride;
+    r.heads = x == nullptr ? 0 : static_cast<int32_t>(x->heads);
+    return r;
+}
+
+int32_t log2_of(int32_t v)
+{
+    int32_t s = 0;
+    while ((1 << s) < v)
+        ++s;
+    return s;
+}
+
+attn::BatchView batch_view(const nvfp4_kv_batch *b, const nvfp4_kv_pages *c, int64_t tokens)
+{
+    attn::BatchView v;
+    v.table = b->page_table;
+    v.cu = b->cu_tokens;
+    v.lens = b->seq_lens;
+    v.table_stride = b->table_stride;
+    v.num_seqs = b->num_seqs;
+    v.max_pages = b->max_pages;
+    v.page_shift = log2_of(c->page_size);
+    v.tokens = static_cast<int32_t>(tokens);
+    v.num_pages = c->num_pages;
+    return v;
+}
+
+// Tokens of a block of the row kernels: several once every SM has blocks
+// enough, so that the block's angles cost one wave of its threads.
+int block_tokens(int64_t tokens, int sm_count)
+{
+    return tokens >= int64_t(sm_count) * 8 * attn::BLOCK_TOKENS ? attn::BLOCK_TOKENS : 1;
+}
+
+}  // namespace
+
+extern "C" int nvfp4_qk_norm_rope(const nvfp4_heads *q, const nvfp4_heads *k, const nvfp4_heads *q_out,
+                                  const nvfp4_heads *k_out, int64_t tokens, int64_t head_dim, const int32_t *positions,
+                                  const nvfp4_norm_rope *norm_rope, void *stream)
+{
+    int rc = check_tokens(tokens);
+    if (rc == NVFP4_OK)
+        rc = check_head_dim(head_dim);
+    if (rc == NVFP4_OK)
+        rc = check_norm_rope(norm_rope, head_dim);
+    if (rc == NVFP4_OK)
+        rc = check_heads(q, tokens);
+    if (rc == NVFP4_OK)
+        rc = check_heads(q_out, tokens);
+    if (rc != NVFP4_OK)
+        return rc;
+    if (q_out->heads != q->heads || (k == nullptr) != (k_out == nullptr) ||
+        (k != nullptr && k->heads != k_out->heads) ||
+        (tokens > 0 && norm_rope->rotary_dim > 0 && positions == nullptr))
+        return NVFP4_ERR_INVALID_ARG;
+    if (k != nullptr) {
+        rc = check_heads(k, tokens);
+        if (rc == NVFP4_OK)
+            rc = check_heads(k_out, tokens);
+        if (rc != NVFP4_OK)
+            return rc;
+    }
+    if (!aligned(positions, 4))
+        return NVFP4_ERR_MISALIGNED;
+    if (tokens == 0)
+        return NVFP4_OK;
+    nvfp4::host::Device d;
+    rc = nvfp4::host::device(&d);
+    if (rc != NVFP4_OK)
+        return rc;
+    attn::NormRopeParams p;
+    p.in[0] = rows_of(q);
+    p.in[1] = rows_of(k);
+    p.out[0] = rows_of(q_out);
+    p.out[1] = rows_of(k_out);
+    p.weight[0] = static_cast<const uint16_t *>(norm_rope->q_weight);
+    p.weight[1] = static_cast<const uint16_t *>(norm_rope->k_weight);
+    p.positions = positions;
+    p.inv_freq = norm_rope->inv_freq;
+    p.half = norm_rope->rotary_dim / 2;
+    p.eps = norm_rope->eps;
+    p.one = (norm_rope->flags & NVFP4_NORM_PLUS_ONE) ? 1.0f : 0.0f;
+    p.tokens = static_cast<int32_t>(tokens);
+    p.block_tokens = block_tokens(tokens, d.sm_count);
+    const dim3 grid(static_cast<unsigned>(cdiv(tokens, p.block_tokens)));
+    launch(head_dim == 256 ? attn::qk_norm_rope_kernel<256> : attn::qk_norm_rope_kernel<128>, grid,
+           dim3(attn::ROW_THREADS), 0, static_cast<cudaStream_t>(stream), p);
+    nvfp4::host::count_launch();
+    return launch_ok();
+}
+
+extern "C" int nvfp4_fp8_kv_append(const nvfp4_heads *k, const nvfp4_heads *v, int64_t tokens,
+                                   const nvfp4_kv_pages *cache, const nvfp4_kv_batch *batch, const int32_t *positions,
+                                   const nvfp4_norm_rope *norm_rope, void *stream)
+{
+    int rc = check_tokens(tokens);
+    if (rc == NVFP4_OK)
+        rc = check_pages(cache);
+    if (rc == NVFP4_OK)
+        rc = check_batch(batch, cache->page_size);
+    if (rc == NVFP4_OK)
+        rc = check_norm_rope(norm_rope, cache->head_dim);
+    if (rc == NVFP4_OK)
+        rc = check_heads(k, tokens);
+    if (rc == NVFP4_OK)
+        rc = check_heads(v, tokens);
+    if (rc != NVFP4_OK)
+        return rc;
+    if (k->heads != cache->kv_heads || v->heads != cache->kv_heads)
+        return NVFP4_ERR_INVALID_ARG;
+    if (!aligned(positions, 4))
+        return NVFP4_ERR_MISALIGNED;
+    if (tokens == 0 || batch->num_seqs == 0)
+        return NVFP4_OK;
+    nvfp4::host::Device d;
+    rc = nvfp4::host::device(&d);
+    if (rc != NVFP4_OK)
+        return rc;
+    attn::AppendParams p;
+    p.in[0] = rows_of(k);
+    p.in[1] = rows_of(v);
+    p.pages[0] = static_cast<uint8_t *>(cache->k_pages);
+    p.pages[1] = static_cast<uint8_t *>(cache->v_pages);
+    p.scale[0] = cache->k_scale;
+    p.scale[1] = cache->v_scale;
+    p.page_stride[0] = cache->k_page_stride;
+    p.page_stride[1] = cache->v_page_stride;
+    p.token_stride[0] = cache->k_token_stride;
+    p.token_stride[1] = cache->v_token_stride;
+    p.head_stride[0] = cache->k_head_stride;
+    p.head_stride[1] = cache->v_head_stride;
+    p.weight = static_cast<const uint16_t *>(norm_rope->k_weight);
+    p.positions = positions;
+    p.inv_freq = norm_rope->inv_freq;
+    p.half = norm_rope->rotary_dim / 2;
+    p.eps = norm_rope->eps;
+    p.one = (norm_rope->flags & NVFP4_NORM_PLUS_ONE) ? 1.0f : 0.0f;
+    p.block_tokens = block_tokens(tokens, d.sm_count);
+    p.batch = batch_view(batch, cache, tokens);
+    p.status = d.status;
+    const dim3 grid(static_cast<unsigned>(cdiv(tokens, p.block_tokens)));
+    launch(cache->head_dim == 256 ? attn::kv_append_kernel<256> : attn::kv_append_kernel<128>, grid,
+           dim3(attn::ROW_THREADS), 0, static_cast<cudaStream_t>(stream), p);
+    nvfp4::host::count_launch();
+    return launch_ok();
+}
+
+extern "C" size_t nvfp4_fp8_kv_attention_workspace_bytes(int64_t tokens, int64_t q_heads, int64_t kv_heads,
+                                                         int64_t head_dim)
+{
+    if (check_tokens(tokens) != NVFP4_OK || check_head_dim(head_dim) != NVFP4_OK || q_heads < 1 || kv_heads < 1 ||
+        q_heads > kMaxHeads || q_heads % kv_heads != 0 || q_heads / kv_heads > 128)
+        return 0;
+    return 256;
+}
+
+extern "C" int nvfp4_fp8_kv_attention(const nvfp4_heads *q, const nvfp4_heads *gate, const nvfp4_heads *out,
+                                      int64_t tokens, const nvfp4_kv_pages *cache, const nvfp4_kv_batch *batch,
+                                      const nvfp4_attention_opts *opts, uint32_t *out_amax, void *ws, size_t ws_bytes,
+                                      void *stream)
+{
+    int rc = check_tokens(tokens);
+    if (rc == NVFP4_OK)
+        rc = check_pages(cache);
+    if (rc == NVFP4_OK)
+        rc = check_batch(batch, cache->page_size);
+    if (rc == NVFP4_OK)
+        rc = check_heads(q, tokens);
+    if (rc == NVFP4_OK)
+        rc = check_heads(out, tokens);
+    if (rc == NVFP4_OK && gate != nullptr)
+        rc = check_heads(gate, tokens);
+    if (rc != NVFP4_OK)
+        return rc;
+    if (opts == nullptr || opts->flags != 0 || !(opts->softmax_scale > 0.0f) || !std::isfinite(opts->softmax_scale) ||
+        out->heads != q->heads || (gate != nullptr && gate->heads != q->heads))
+        return NVFP4_ERR_INVALID_ARG;
+    if (q->heads % cache->kv_heads != 0 || q->heads / cache->kv_heads > 128)
+        return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned(out_amax, 4) || !aligned(ws, 16))
+        return NVFP4_ERR_MISALIGNED;
+    if (ws == nullptr ||
+        ws_bytes < nvfp4_fp8_kv_attention_workspace_bytes(tokens, q->heads, cache->kv_heads, cache->head_dim))
+        return NVFP4_ERR_WORKSPACE;
+    nvfp4::host::Device d;
+    rc = nvfp4::host::device(&d);
+    if (rc != NVFP4_OK)
+        return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (out_amax != nullptr) {
+        rc = nvfp4::host::clear_words(out_amax, 1, s);
+        if (rc != NVFP4_OK)
+            return rc;
+    }
+    if (tokens == 0 || batch->num_seqs == 0)
+        return NVFP4_OK;
+    attn::AttnParams p;
+    p.q = rows_of(q);
+    p.gate = rows_of(gate);
+    p.out = rows_of(out);
+    p.k_pages = static_cast<const uint8_t *>(cache->k_pages);
+    p.v_pages = static_cast<const uint8_t *>(cache->v_pages);
+    p.k_page_stride = cache->k_page_stride;
+    p.k_token_stride = cache->k_token_stride;
+    p.k_head_stride = cache->k_head_stride;
+    p.v_page_stride = cache->v_page_stride;
+    p.v_token_stride = cache->v_token_stride;
+    p.v_head_stride = cache->v_head_stride;
+    p.k_scale = cache->k_scale;
+    p.v_scale = cache->v_scale;
+    p.kv_heads = cache->kv_heads;
+    p.group = static_cast<int32_t>(q->heads / cache->kv_heads);
+    p.softmax_scale = opts->softmax_scale;
+    p.batch = batch_view(batch, cache, tokens);
+    p.out_amax = out_amax;
+    p.status = d.status;
+    const dim3 grid(static_cast<unsigned>(tokens), static_cast<unsigned>(q->heads));
+    launch(cache->head_dim == 256 ? attn::paged_attention_simple_kernel<256> : attn::paged_attention_simple_kernel<128>,
+           grid, dim3(128), 0, s, p);
+    nvfp4::host::count_launch();
+    return launch_ok();
+}

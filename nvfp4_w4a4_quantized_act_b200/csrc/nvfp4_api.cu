@@ -14,6 +14,7 @@
 #include "nvfp4.h"
 #include "gemm_kernel.cuh"
 #include "gemm_pair_kernel.cuh"
+#include "host.h"
 #include "kv_cache_kernels.cuh"
 #include "quantize_kernels.cuh"
 
@@ -38,9 +39,7 @@ struct DeviceState {
 DeviceState g_dev[kMaxDevices];
 std::mutex g_mu;
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+using nvfp4::host::EncodeTiledFn;
 EncodeTiledFn g_encode = nullptr;
 
 // Looks up (once per device) the SM count, the status word address and
@@ -112,36 +111,9 @@ int check_segments(const nvfp4_segment *segs, int nseg, int64_t N, nvfp4::SegRow
     return expect == N ? NVFP4_OK : NVFP4_ERR_INVALID_ARG;
 }
 
-thread_local bool t_launch_failed = false;
+using nvfp4::host::launch;
 
-// Launches a kernel with programmatic stream serialization: the kernel may
-// be scheduled while the previous kernel on the stream is still running and
-// waits for it (griddepcontrol.wait) before touching global memory.  Every
-// kernel of this library does that wait first, so stream order holds.
-template <typename... KArgs, typename... Args>
-void launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, Args... args)
-{
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg;
-    std::memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess)
-        t_launch_failed = true;
-}
-
-int launch_ok()
-{
-    const bool failed = t_launch_failed;
-    t_launch_failed = false;
-    return (cudaGetLastError() == cudaSuccess && !failed) ? NVFP4_OK : NVFP4_ERR_CUDA;
-}
+int launch_ok() { return nvfp4::host::launch_failed() ? NVFP4_ERR_CUDA : NVFP4_OK; }
 
 // Clears `n` amax words on the stream (a kernel, so that the launches around
 // it keep their programmatic dependencies).
@@ -832,6 +804,8 @@ int nvfp4_get_status(void *stream)
         return NVFP4_ERR_TIMEOUT;
     if (v & nvfp4::kStatusNonFinite)
         return NVFP4_ERR_NONFINITE;
+    if (v & nvfp4::kStatusBadIndex)
+        return NVFP4_ERR_INVALID_ARG;
     return NVFP4_OK;
 }
 
@@ -1144,3 +1118,28 @@ extern "C" int nvfp4_fp8_kv_quantize(const void *X, int64_t rows, int64_t cols, 
     g_launches++;
     return launch_ok();
 }
+
+// ---------------------------------- services for the attention entry points
+
+namespace nvfp4 {
+namespace host {
+
+int device(Device *out)
+{
+    DeviceState *d = device_state();
+    if (d == nullptr)
+        return NVFP4_ERR_CUDA;
+    if (!d->supported)
+        return NVFP4_ERR_NO_DEVICE;
+    out->sm_count = d->sm_count;
+    out->status = d->status;
+    out->encode_tiled = g_encode;
+    return NVFP4_OK;
+}
+
+void count_launch() { g_launches++; }
+
+int clear_words(uint32_t *words, int n, cudaStream_t stream) { return zero_words(words, n, stream); }
+
+}  // namespace host
+}  // namespace nvfp4

@@ -25,12 +25,11 @@
 
 #include "fp_div.cuh"
 #include "ptx_sm100.cuh"
+#include "status.cuh"
 
 namespace nvfp4 {
 
 constexpr int kMaxSeg = 16;
-constexpr uint32_t kStatusTimeout = 1u;
-constexpr uint32_t kStatusNonFinite = 2u;
 
 // Rows [0, end[0]) belong to segment 0, [end[i-1], end[i]) to segment i.
 struct SegRows {

@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(_PKG, "libnvfp4.so")
 NVFP4_STATIC_SCALE = 1
 NVFP4_OUT_FP32 = 2
 NVFP4_AMAX_GIVEN = 4
+NVFP4_NORM_PLUS_ONE = 8
 NVFP4_DEBUG_INJECT_STALL = 1 << 30
 NVFP4_SINGLE_CTA = 1 << 29
 MAX_SEGMENTS = 16
@@ -37,6 +38,7 @@ EXPORTED = [
     "nvfp4_device_supported", "nvfp4_launch_count", "nvfp4_linear_fused_noalloc",
     "nvfp4_quantize_weights_gated", "nvfp4_linear_swiglu", "nvfp4_gemm_prequant_swiglu",
     "nvfp4_fp8_kv_calibrate", "nvfp4_fp8_kv_quantize",
+    "nvfp4_qk_norm_rope", "nvfp4_fp8_kv_append", "nvfp4_fp8_kv_attention", "nvfp4_fp8_kv_attention_workspace_bytes",
 ]
 
 
@@ -48,6 +50,33 @@ class Nvfp4Error(RuntimeError):
 
 class Segment(ctypes.Structure):
     _fields_ = [("n_begin", ctypes.c_int64), ("n_end", ctypes.c_int64)]
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("heads", ctypes.c_int64)]
+
+
+class KvPages(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("k_page_stride", ctypes.c_int64), ("k_token_stride", ctypes.c_int64),
+                ("k_head_stride", ctypes.c_int64), ("v_page_stride", ctypes.c_int64),
+                ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64), ("num_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class KvBatch(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("cu_tokens", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("num_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
+class NormRope(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p),
+                ("rotary_dim", ctypes.c_int32), ("eps", ctypes.c_float), ("flags", ctypes.c_uint)]
+
+
+class AttentionOpts(ctypes.Structure):
+    _fields_ = [("softmax_scale", ctypes.c_float), ("flags", ctypes.c_uint)]
 
 
 _lib = None
@@ -91,6 +120,10 @@ def lib() -> ctypes.CDLL:
         "nvfp4_gemm_prequant_swiglu": (ctypes.c_int, [u8p, u8p, fp, i64, i64, u8p, u8p, i64, fp, vp, vp, sz, vp]),
         "nvfp4_fp8_kv_calibrate": (ctypes.c_int, [vp, i64, i64, i64, fp, vp, sz, vp]),
         "nvfp4_fp8_kv_quantize": (ctypes.c_int, [vp, i64, i64, i64, fp, u8p, i64, vp]),
+        "nvfp4_qk_norm_rope": (ctypes.c_int, [vp, vp, vp, vp, i64, i64, vp, vp, vp]),
+        "nvfp4_fp8_kv_append": (ctypes.c_int, [vp, vp, i64, vp, vp, vp, vp, vp]),
+        "nvfp4_fp8_kv_attention_workspace_bytes": (sz, [i64, i64, i64, i64]),
+        "nvfp4_fp8_kv_attention": (ctypes.c_int, [vp, vp, vp, i64, vp, vp, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -497,4 +530,186 @@ def fp8_kv_quantize(X: torch.Tensor, scale: torch.Tensor, out=None, stream=None)
                          f"(got {out.dtype}, shape {tuple(out.shape)}, strides {out.stride()})")
     _check(lib().nvfp4_fp8_kv_quantize(_p(X), rows, cols, X.stride(0), _p(scale), _p(out), out.stride(0),
                                        _stream(stream)), "nvfp4_fp8_kv_quantize")
+    return out
+
+
+# ------------------------------------- attention over the paged FP8 KV cache
+
+_byref = ctypes.byref
+
+
+def _same_device(*ts):
+    """All tensors lie on the current device: the library launches there."""
+    _require_cuda(*ts)
+    dev = None
+    for t in ts:
+        if t is not None:
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError(f"tensors on different devices ({dev} and {t.device})")
+    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {dev}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _heads(t, name, like=None, written=False):
+    """Head rows of a bf16 [tokens, heads, head_dim] tensor or view as the
+    library's struct; `like`: the tensor whose shape it must have; `written`:
+    no two of its rows may overlap."""
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] != 1):
+        raise ValueError(f"{name} must be a bf16 [tokens, heads, head_dim] tensor with unit stride along head_dim "
+                         f"(got {t.dtype}, shape {tuple(t.shape)}, strides {t.stride()})")
+    T, H, D = t.shape
+    if like is not None and t.shape != like.shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(like.shape)}")
+    st, sh = t.stride(0) if T > 1 else H * D, t.stride(1) if H > 1 else D
+    if written and not ((sh >= D and (T == 1 or st >= (H - 1) * sh + D)) or
+                        (st >= D and sh >= (T - 1) * st + D)):
+        raise ValueError(f"{name}'s rows overlap (shape {tuple(t.shape)}, strides {t.stride()})")
+    return Heads(t.data_ptr(), st, sh, H)
+
+
+def _vector(t, name, dtype, n=None):
+    if t.dtype != dtype or t.dim() != 1 or (t.shape[0] > 1 and t.stride(0) != 1) or (n is not None and t.shape[0] < n):
+        raise ValueError(f"{name} must be a contiguous {dtype} vector{'' if n is None else f' of at least {n}'} "
+                         f"(got {t.dtype}, shape {tuple(t.shape)}, strides {t.stride()})")
+    return t.data_ptr()
+
+
+def _norm_rope(head_dim, inv_freq, q_weight, k_weight, eps, plus_one):
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and (w.dtype != torch.bfloat16 or w.shape != (head_dim,) or w.stride(0) != 1):
+            raise ValueError(f"{name} must be a contiguous bf16 [{head_dim}] tensor (got {w.dtype}, {tuple(w.shape)})")
+    return NormRope(None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
+                    None if inv_freq is None else _vector(inv_freq, "inv_freq", torch.float32),
+                    0 if inv_freq is None else 2 * inv_freq.shape[0], eps, NVFP4_NORM_PLUS_ONE if plus_one else 0)
+
+
+def _page_strides(t):
+    """Byte strides of pages, rows and heads; a dimension of one element gets
+    a stride that nests with the others (torch leaves it arbitrary)."""
+    row = t.stride(1)
+    head = t.stride(2) if t.shape[2] > 1 else row
+    return t.stride(0) if t.shape[0] > 1 else max(row * t.shape[1], head * t.shape[2]), row, head
+
+
+def _kv_pages(k_pages, v_pages, k_scale, v_scale):
+    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        if t.dtype != torch.uint8 or t.dim() != 4 or t.stride(3) != 1 or t.shape != k_pages.shape:
+            raise ValueError(f"{name} must be a uint8 [pages, page_size, kv_heads, head_dim] tensor with unit stride "
+                             f"along head_dim, both of one shape (got {t.dtype}, {tuple(t.shape)}, {t.stride()})")
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if t.dtype != torch.float32 or t.numel() != 1:
+            raise ValueError(f"{name} must hold one fp32 value")
+    n, size, heads, dim = k_pages.shape
+    return KvPages(k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                   *_page_strides(k_pages), *_page_strides(v_pages), n, size, heads, dim)
+
+
+def _kv_batch(page_table, cu_tokens, seq_lens):
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or \
+            (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError(f"page_table must be an int32 [sequences, pages] tensor with unit stride along pages "
+                         f"(got {page_table.dtype}, {tuple(page_table.shape)}, {page_table.stride()})")
+    B, P = page_table.shape
+    return KvBatch(page_table.data_ptr(), _vector(cu_tokens, "cu_tokens", torch.int32, B + 1),
+                   _vector(seq_lens, "seq_lens", torch.int32, B), page_table.stride(0) if B > 1 else P, B, P)
+
+
+def _new(stream, *size, dtype, device):
+    """An output or scratch tensor for a call on `stream` (None: the current
+    one); the allocator must know when that is another stream."""
+    t = torch.empty(size, dtype=dtype, device=device)
+    if stream is not None and t.is_cuda:
+        t.record_stream(stream)
+    return t
+
+
+def qk_norm_rope(q, k, positions, inv_freq=None, q_weight=None, k_weight=None, eps=1e-6, plus_one=False, q_out=None,
+                 k_out=None, stream=None):
+    """nvfp4_qk_norm_rope -> (q_out, k_out): norm and rotation of every query
+    and key head.  q, k: bf16 [tokens, heads, head_dim] views (k may be None);
+    positions: int32 [tokens]; inv_freq: fp32 [rotary_dim / 2] (None: no
+    rotation); weights: bf16 [head_dim] (None: no norm; plus_one: 1 + w).  An
+    output may be its input."""
+    _same_device(q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out)
+    hq = _heads(q, "q")
+    T, _, D = q.shape
+    hk = hko = None
+    if q_out is None:
+        q_out = _new(stream, *q.shape, dtype=torch.bfloat16, device=q.device)
+    hqo = _heads(q_out, "q_out", q, written=True)
+    if k is not None:
+        hk = _heads(k, "k")
+        if k.shape[0] != T or k.shape[2] != D:
+            raise ValueError(f"k has shape {tuple(k.shape)}, q {tuple(q.shape)}")
+        if k_out is None:
+            k_out = _new(stream, *k.shape, dtype=torch.bfloat16, device=q.device)
+        hko = _heads(k_out, "k_out", k, written=True)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    if inv_freq is not None and positions is None:
+        raise ValueError("a rotation needs positions")
+    nr = _norm_rope(D, inv_freq, q_weight, k_weight, eps, plus_one)
+    _check(lib().nvfp4_qk_norm_rope(_byref(hq), None if hk is None else _byref(hk), _byref(hqo),
+                                    None if hko is None else _byref(hko), T, D,
+                                    None if positions is None else _vector(positions, "positions", torch.int32, T),
+                                    _byref(nr), _stream(stream)), "nvfp4_qk_norm_rope")
+    return q_out, k_out
+
+
+def fp8_kv_append(k, v, k_pages, v_pages, k_scale, v_scale, page_table, cu_tokens, seq_lens, inv_freq=None,
+                  k_weight=None, eps=1e-6, plus_one=False, positions=None, stream=None):
+    """nvfp4_fp8_kv_append: the batch's new keys (normalised and rotated on the
+    way) and values, bf16 [tokens, kv_heads, head_dim], as E4M3 codes into the
+    pages of their sequences (see nvfp4_kv_batch).  Pages: uint8 [pages,
+    page_size, kv_heads, head_dim], any nested strides; scales: fp32 [1]."""
+    _same_device(k, v, k_pages, v_pages, k_scale, v_scale, page_table, cu_tokens, seq_lens, inv_freq, k_weight,
+                 positions)
+    hk, hv = _heads(k, "k"), _heads(v, "v", k)
+    T, H, D = k.shape
+    pages = _kv_pages(k_pages, v_pages, k_scale, v_scale)
+    if (H, D) != tuple(k_pages.shape[2:]):
+        raise ValueError(f"k has shape {tuple(k.shape)}, the pages {tuple(k_pages.shape)}")
+    batch = _kv_batch(page_table, cu_tokens, seq_lens)
+    nr = _norm_rope(D, inv_freq, None, k_weight, eps, plus_one)
+    _check(lib().nvfp4_fp8_kv_append(_byref(hk), _byref(hv), T, _byref(pages), _byref(batch),
+                                     None if positions is None else _vector(positions, "positions", torch.int32, T),
+                                     _byref(nr), _stream(stream)), "nvfp4_fp8_kv_append")
+
+
+def fp8_kv_attention_workspace_bytes(tokens: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(lib().nvfp4_fp8_kv_attention_workspace_bytes(tokens, q_heads, kv_heads, head_dim))
+
+
+def fp8_kv_attention(q, k_pages, v_pages, k_scale, v_scale, page_table, cu_tokens, seq_lens, softmax_scale=None,
+                     gate=None, out=None, out_amax=None, ws=None, stream=None):
+    """nvfp4_fp8_kv_attention -> out: causal attention of the batch's new
+    tokens, q bf16 [tokens, q_heads, head_dim], over their sequences' pages,
+    times sigmoid(gate).  softmax_scale defaults to head_dim ** -0.5; out_amax
+    (4 bytes, e.g. the first word of a quantize workspace) receives max|out|
+    for quantize_act(..., amax_given=True)."""
+    _same_device(q, k_pages, v_pages, k_scale, v_scale, page_table, cu_tokens, seq_lens, gate, out, out_amax, ws)
+    hq = _heads(q, "q")
+    T, H, D = q.shape
+    pages = _kv_pages(k_pages, v_pages, k_scale, v_scale)
+    Hk = k_pages.shape[2]
+    if D != k_pages.shape[3] or Hk == 0 or H % Hk:
+        raise ValueError(f"q has shape {tuple(q.shape)}, the pages {tuple(k_pages.shape)}")
+    batch = _kv_batch(page_table, cu_tokens, seq_lens)
+    hg = None if gate is None else _heads(gate, "gate", q)
+    if out is None:
+        out = _new(stream, T, H, D, dtype=torch.bfloat16, device=q.device)
+    ho = _heads(out, "out", q, written=True)
+    L = lib()
+    need = L.nvfp4_fp8_kv_attention_workspace_bytes(T, H, Hk, D)
+    if ws is None:
+        ws = _new(stream, max(need, 16), dtype=torch.uint8, device=q.device)
+    _buffer(ws, need, "ws")
+    if out_amax is not None:
+        _buffer(out_amax, 4, "out_amax")
+    opts = AttentionOpts(D ** -0.5 if softmax_scale is None else softmax_scale, 0)
+    _check(L.nvfp4_fp8_kv_attention(_byref(hq), None if hg is None else _byref(hg), _byref(ho), T, _byref(pages),
+                                    _byref(batch), _byref(opts), _p(out_amax), _p(ws), _nbytes(ws), _stream(stream)),
+           "nvfp4_fp8_kv_attention")
     return out
