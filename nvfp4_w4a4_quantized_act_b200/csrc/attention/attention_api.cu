@@ -2,6 +2,7 @@
 // norms and rotation, the paged FP8 cache's append, attention over it.
 // Argument checks and launches; declared and documented in include/nvfp4.h.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -11,7 +12,7 @@
 #include "nvfp4.h"
 #include "head_rows_kernels.cuh"
 #include "host.h"
-#include "paged_attention_simple.cuh"
+#include "paged_attention_kernel.cuh"
 #include "paged_batch.cuh"
 
 namespace {
@@ -145,6 +146,64 @@ attn::BatchView batch_view(const nvfp4_kv_batch *b, const nvfp4_kv_pages *c, int
     return v;
 }
 
+// The pages of K or V as a 4-D byte tensor, dimensions in the order of their
+// strides behind the contiguous head_dim; row_at and head_at say where the
+// page's rows and the heads ended up.  A box is one page's rows (128 at most)
+// by 128 bytes of one head.
+int make_page_map(const nvfp4::host::Device &d, CUtensorMap *map, const void *base, const nvfp4_kv_pages *c,
+                  int64_t page_stride, int64_t row_stride, int64_t head_stride, int32_t *row_at, int32_t *head_at)
+{
+    struct Dim {
+        int64_t stride, size;
+        int which;  // 0 row, 1 head, 2 page
+    } dims[3] = {{row_stride, c->page_size, 0}, {head_stride, c->kv_heads, 1}, {page_stride, c->num_pages, 2}};
+    std::sort(dims, dims + 3, [](const Dim &a, const Dim &b) {
+        return a.stride != b.stride ? a.stride < b.stride : a.which < b.which;
+    });
+    cuuint64_t size[4] = {static_cast<cuuint64_t>(c->head_dim), 0, 0, 0};
+    cuuint64_t stride[3];
+    cuuint32_t box[4] = {128, 1, 1, 1}, unit[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 3; ++i) {
+        size[i + 1] = static_cast<cuuint64_t>(dims[i].size);
+        stride[i] = static_cast<cuuint64_t>(dims[i].stride);
+        if (dims[i].which == 0) {
+            box[i + 1] = static_cast<cuuint32_t>(std::min(c->page_size, attn::KEY_BLOCK));
+            *row_at = i + 1;
+        } else if (dims[i].which == 1) {
+            *head_at = i + 1;
+        }
+    }
+    const CUresult r = d.encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(base), size, stride, box,
+                                      unit, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? NVFP4_OK : NVFP4_ERR_CUDA;
+}
+
+// Shared memory beyond the default, once per device.
+int allow_smem(int device)
+{
+    static std::atomic<bool> done[64];
+    if (device < 0 || device >= 64)
+        return NVFP4_ERR_CUDA;
+    if (done[device].load(std::memory_order_acquire))
+        return NVFP4_OK;
+    if (cudaFuncSetAttribute(attn::paged_attention_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             attn::attn_smem_bytes<128>()) != cudaSuccess ||
+        cudaFuncSetAttribute(attn::paged_attention_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             attn::attn_smem_bytes<256>()) != cudaSuccess)
+        return NVFP4_ERR_CUDA;
+    done[device].store(true, std::memory_order_release);
+    return NVFP4_OK;
+}
+
+// Workspace: a PartInfo per CTA, then the two parts of each CTA: per row its
+// reference and sum, then its sums of values.
+constexpr int64_t kPartsBytes = (attn::CTAS * sizeof(attn::PartInfo) + 255) / 256 * 256;
+
+int64_t part_rows(int64_t tokens, int64_t group) { return std::min<int64_t>(attn::ROW_TILE / group, tokens) * group; }
+
+int64_t part_ml_bytes(int64_t rows) { return (attn::CTAS * 2 * rows * 8 + 255) / 256 * 256; }
+
 // Tokens of a block of the row kernels: several once every SM has blocks
 // enough, so that the block's angles cost one wave of its threads.
 int block_tokens(int64_t tokens, int sm_count)
@@ -271,7 +330,8 @@ extern "C" size_t nvfp4_fp8_kv_attention_workspace_bytes(int64_t tokens, int64_t
     if (check_tokens(tokens) != NVFP4_OK || check_head_dim(head_dim) != NVFP4_OK || q_heads < 1 || kv_heads < 1 ||
         q_heads > kMaxHeads || q_heads % kv_heads != 0 || q_heads / kv_heads > 128)
         return 0;
-    return 256;
+    const int64_t rows = part_rows(tokens, q_heads / kv_heads);
+    return static_cast<size_t>(kPartsBytes + part_ml_bytes(rows) + attn::CTAS * 2 * rows * head_dim * 4);
 }
 
 extern "C" int nvfp4_fp8_kv_attention(const nvfp4_heads *q, const nvfp4_heads *gate, const nvfp4_heads *out,
@@ -314,29 +374,42 @@ extern "C" int nvfp4_fp8_kv_attention(const nvfp4_heads *q, const nvfp4_heads *g
     }
     if (tokens == 0 || batch->num_seqs == 0)
         return NVFP4_OK;
+    CUtensorMap tm_k, tm_v;
     attn::AttnParams p;
+    if (make_page_map(d, &tm_k, cache->k_pages, cache, cache->k_page_stride, cache->k_token_stride,
+                      cache->k_head_stride, &p.k_row_at, &p.k_head_at) != NVFP4_OK ||
+        make_page_map(d, &tm_v, cache->v_pages, cache, cache->v_page_stride, cache->v_token_stride,
+                      cache->v_head_stride, &p.v_row_at, &p.v_head_at) != NVFP4_OK ||
+        allow_smem(d.index) != NVFP4_OK)
+        return NVFP4_ERR_CUDA;
     p.q = rows_of(q);
     p.gate = rows_of(gate);
     p.out = rows_of(out);
-    p.k_pages = static_cast<const uint8_t *>(cache->k_pages);
-    p.v_pages = static_cast<const uint8_t *>(cache->v_pages);
-    p.k_page_stride = cache->k_page_stride;
-    p.k_token_stride = cache->k_token_stride;
-    p.k_head_stride = cache->k_head_stride;
-    p.v_page_stride = cache->v_page_stride;
-    p.v_token_stride = cache->v_token_stride;
-    p.v_head_stride = cache->v_head_stride;
     p.k_scale = cache->k_scale;
     p.v_scale = cache->v_scale;
     p.kv_heads = cache->kv_heads;
     p.group = static_cast<int32_t>(q->heads / cache->kv_heads);
+    p.tile_tokens = attn::ROW_TILE / p.group;
     p.softmax_scale = opts->softmax_scale;
     p.batch = batch_view(batch, cache, tokens);
+    p.part_rows = static_cast<int32_t>(part_rows(tokens, p.group));
+    uint8_t *base = static_cast<uint8_t *>(ws);
+    p.parts = reinterpret_cast<attn::PartInfo *>(base);
+    p.part_ml = reinterpret_cast<float *>(base + kPartsBytes);
+    p.part_o = reinterpret_cast<float *>(base + kPartsBytes + part_ml_bytes(p.part_rows));
     p.out_amax = out_amax;
     p.status = d.status;
-    const dim3 grid(static_cast<unsigned>(tokens), static_cast<unsigned>(q->heads));
-    launch(cache->head_dim == 256 ? attn::paged_attention_simple_kernel<256> : attn::paged_attention_simple_kernel<128>,
-           grid, dim3(128), 0, s, p);
+    const dim3 join_grid(attn::CTAS, static_cast<unsigned>(cdiv(p.part_rows, attn::JOIN_ROWS)));
+    if (cache->head_dim == 256) {
+        launch(attn::paged_attention_kernel<256>, dim3(attn::CTAS), dim3(attn::ATTN_THREADS),
+               attn::attn_smem_bytes<256>(), s, tm_k, tm_v, p);
+        launch(attn::paged_attention_join_kernel<256>, join_grid, dim3(attn::JOIN_ROWS * 32), 0, s, p);
+    } else {
+        launch(attn::paged_attention_kernel<128>, dim3(attn::CTAS), dim3(attn::ATTN_THREADS),
+               attn::attn_smem_bytes<128>(), s, tm_k, tm_v, p);
+        launch(attn::paged_attention_join_kernel<128>, join_grid, dim3(attn::JOIN_ROWS * 32), 0, s, p);
+    }
+    nvfp4::host::count_launch();
     nvfp4::host::count_launch();
     return launch_ok();
 }

@@ -52,6 +52,7 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 struct Device {
+    int index;
     int sm_count;
     uint32_t *status;  // device address of the status word
     EncodeTiledFn encode_tiled;

@@ -1131,6 +1131,7 @@ int device(Device *out)
         return NVFP4_ERR_CUDA;
     if (!d->supported)
         return NVFP4_ERR_NO_DEVICE;
+    out->index = static_cast<int>(d - g_dev);
     out->sm_count = d->sm_count;
     out->status = d->status;
     out->encode_tiled = g_encode;
