@@ -390,6 +390,7 @@ extern "C" int nvfp4_fp8_kv_attention(const nvfp4_heads *q, const nvfp4_heads *g
     p.kv_heads = cache->kv_heads;
     p.group = static_cast<int32_t>(q->heads / cache->kv_heads);
     p.tile_tokens = attn::ROW_TILE / p.group;
+    p.group_inv = static_cast<uint32_t>((65536 + p.group - 1) / p.group);
     p.softmax_scale = opts->softmax_scale;
     p.batch = batch_view(batch, cache, tokens);
     p.part_rows = static_cast<int32_t>(part_rows(tokens, p.group));

@@ -27,12 +27,14 @@ struct SeqItems {
     Seq s;
     int32_t tiles;  // row tiles
     int32_t past;   // len - fresh (may be negative)
+    int32_t m0;     // first row tile with keys by the formula of cost()
 
     __device__ __forceinline__ void set(const Seq &seq, int tile_tokens)
     {
         s = seq;
         tiles = (seq.fresh + tile_tokens - 1) / tile_tokens;
         past = seq.len - seq.fresh;
+        m0 = past >= 0 ? 0 : -past / tile_tokens;
     }
 
     // Cost of row tile m, and of all row tiles before m.
@@ -42,27 +44,28 @@ struct SeqItems {
     }
     __device__ __forceinline__ int64_t before(int m, int tile_tokens) const
     {
-        // row tiles i with past + tile_tokens * (i + 1) > 0 start at m0
-        const int64_t t = tile_tokens;
-        const int64_t m0 = past >= 0 ? 0 : static_cast<int64_t>(-past) / tile_tokens;
         int64_t sum = static_cast<int64_t>(KEY_BLOCK) * m;
         if (m > m0) {
             const int64_t n = m - m0;
-            sum += n * past + t * (n * m0 + n * (n + 1) / 2);
+            sum += n * past + tile_tokens * (n * m0 + n * (n + 1) / 2);
         }
         return sum;
     }
     __device__ __forceinline__ int64_t total(int tile_tokens) const { return before(tiles, tile_tokens); }
+};
 
-    // Keys that the last row (and the first) of row tile m sees.
-    __device__ __forceinline__ int keys(int m, int tile_tokens) const
-    {
-        return max(past + min(s.fresh, (m + 1) * tile_tokens), 0);
-    }
-    __device__ __forceinline__ int keys_first(int m, int tile_tokens) const
-    {
-        return max(past + m * tile_tokens + 1, 0);
-    }
+// What the kernel's warps need to know of an item.
+struct Item {
+    int32_t blocks;      // key blocks of this CTA's part; 0: no more items
+    int32_t t0;          // first of them
+    int32_t keys;        // keys that the last row sees
+    int32_t seen_first;  // and the first row
+    int32_t rows;        // rows (tokens x group)
+    int32_t past0;       // position of the first token
+    int32_t token0;      // first token row
+    int32_t head;        // key head
+    int32_t seq;
+    int32_t part;        // 0: the item is this CTA's alone; 1: begun by an earlier CTA; 2: finished by later ones
 };
 
 // A CTA's walk over its part of the line.
@@ -71,48 +74,56 @@ struct Walk {
     int64_t x;     // offset in the item
     int64_t left;  // cost left
     SeqItems q;
-    // the current item
-    int keys, blocks, t0, t1;
 
-    // Moves to the next item with key blocks for this CTA; false at the end.
-    // First call: `b, h, m, x, left, q` set by the start.
-    __device__ __forceinline__ bool next(const BatchView &v, int kv_heads, int tile_tokens, bool first)
+    // The next item with key blocks for this CTA; blocks = 0 at the end.  `end_cost`: for part 2, the cost of the
+    // item behind this CTA's share.
+    __device__ __forceinline__ Item next(const BatchView &v, int kv_heads, int tile_tokens, int group, int64_t &end_cost)
     {
-        if (!first)
-            step(v, kv_heads, tile_tokens);
+        Item it;
+        it.blocks = 0;
         while (left > 0) {
+            if (m >= q.tiles) {
+                m = 0;
+                x = 0;
+                if (++h >= kv_heads) {
+                    h = 0;
+                    bool ignored = false;
+                    do {
+                        if (++b >= v.num_seqs) {
+                            left = 0;
+                            return it;
+                        }
+                        q.set(load_seq(v, b, ignored), tile_tokens);
+                    } while (q.tiles == 0);
+                }
+            }
             const int64_t c = q.cost(m, tile_tokens);
             const int64_t x1 = min(c, x + left);
-            keys = q.keys(m, tile_tokens);
-            blocks = max((keys + KEY_BLOCK - 1) / KEY_BLOCK, 1);
-            t0 = static_cast<int>(x * blocks / c);
-            t1 = static_cast<int>(x1 * blocks / c);
+            const int first = m * tile_tokens;
+            const int tokens = min(q.s.fresh - first, tile_tokens);
+            it.keys = max(q.past + first + tokens, 0);
+            const int blocks = max((it.keys + KEY_BLOCK - 1) / KEY_BLOCK, 1);
+            // in fp64: rounded, but alike for both neighbours of a boundary and never falling as x grows
+            const int t0 = static_cast<int>(static_cast<double>(x) * blocks / static_cast<double>(c));
+            const int t1 = x1 == c ? blocks : static_cast<int>(static_cast<double>(x1) * blocks / static_cast<double>(c));
+            end_cost = c - x1;
             left -= x1 - x;
-            x = x1;
-            if (t1 > t0)
-                return true;
-            step(v, kv_heads, tile_tokens);
+            it.t0 = t0;
+            it.seen_first = max(q.past + first + 1, 0);
+            it.rows = tokens * group;
+            it.past0 = q.past + first;
+            it.token0 = q.s.first + first;
+            it.head = h;
+            it.seq = b;
+            it.part = t0 > 0 ? 1 : t1 < blocks ? 2 : 0;
+            x = 0;
+            ++m;
+            if (t1 > t0) {
+                it.blocks = t1 - t0;
+                return it;
+            }
         }
-        return false;
-    }
-
-private:
-    __device__ __forceinline__ void step(const BatchView &v, int kv_heads, int tile_tokens)
-    {
-        x = 0;
-        if (++m < q.tiles)
-            return;
-        m = 0;
-        if (++h < kv_heads)
-            return;
-        h = 0;
-        bool bad = false;
-        while (left > 0 && ++b < v.num_seqs) {
-            q.set(load_seq(v, b, bad), tile_tokens);
-            if (q.tiles > 0)
-                return;
-        }
-        left = 0;
+        return it;
     }
 };
 

@@ -14,15 +14,18 @@
 //   [128, 256); high = E4M3(x), low = E4M3(x - high).  A bf16 value has 8
 //   significant bits, two E4M3 values 4 each: exact down to 2^-10 of the row's
 //   largest, off by at most 2^-17 of the largest below.
-//   Probabilities: 2^(t - r + 8) with r within a few units of the largest t of
-//   the block of 128 keys, so the block's largest lies in [2^5, 2^8.75];
-//   high keeps 4 significant bits by truncation, low = E4M3(p - high): 8 bits
-//   together, as bf16 would keep, and never coarser than 2^-14 of the block's
-//   largest.  The reference r follows the block's maximum both ways (not only
-//   up, as a running maximum would): after a key far above the rest, a sink,
-//   the others keep their precision.  When r moves, the accumulated row is
-//   rescaled by the exact difference; r never falls more than 40 below the
-//   largest t so far, under which nothing counts in 32 bits anyway.
+//   Probabilities: 2^(t - r + 8); high keeps 4 significant bits by
+//   truncation, low = E4M3(p - high): 8 bits together, as bf16 would keep, but
+//   no finer than 2^-9.  So the reference r has to keep a block's
+//   probabilities up: it follows the blocks of 128 keys both ways, not only
+//   up as a running maximum would (after a key far above the rest, a sink,
+//   the others would lose their bits).  A block's largest may lie 0.75 above r
+//   and 5 below it, or 2 below it where the block before had a sum under 64:
+//   then a block's sum or its neighbour's is at least 64, and 128 errors of
+//   2^-9 stay under 2^-8 of it.  When r moves (to 1 above the block's largest)
+//   the accumulated row is rescaled by the exact difference; the wide window
+//   makes that rare, the bound on the sum keeps it safe.  r never falls more
+//   than 40 below the largest t so far, under which nothing counts in 32 bits.
 //
 // One CTA per SM; query tile of 128 rows (tokens x query heads of one key
 // head) against blocks of 128 keys; work is shared by attention_schedule.cuh.
@@ -31,17 +34,23 @@
 //   warp 1       TMEM; one lane issues the MMAs: scores of block j+1 before
 //                the values of block j, so the softmax of one block runs under
 //                the MMAs of the next
-//   warps 4..11  two threads per row (64 keys each): softmax, probabilities to
-//                TMEM over the scores, rescaling, queries to shared memory,
-//                results
+//   warp 2       walks the CTA's items, four ahead of the others, and brings
+//                their queries and gates into L2
+//   warps 4..7   one thread per row: rescaling of the accumulated rows, values
+//                out of sight, results
+//   warps 8..15  two threads per row (64 keys each): softmax, probabilities to
+//                TMEM over the scores, queries to shared memory
+// The softmax of a block has the time of two products (2 x 1060 cycles at
+// D = 256) before the tensor cores would wait for it; everything that is not
+// on its path is done by other warps beside it.
 // TMEM: D columns of output, two buffers of 128 score columns.  P of a block
 // replaces its scores: high and low terms, four keys per column.
 //
 // Keys out of a row's sight must not reach it whatever they hold: scores are
 // replaced before the maximum; values meet a zero probability, which only a
 // NaN code survives (E4M3 has no infinity), so in blocks that some row does
-// not see to the end the softmax threads clear values that no row sees and
-// NaN codes in the rest, and remember per dimension the first key with a NaN:
+// not see to the end warps 4..7 clear values that no row sees and NaN codes in
+// the rest, and remember per dimension the first key with a NaN:
 // the rows that see it get their NaN when the result is written.
 //
 // Every mbarrier wait is bounded in time; when one runs out the kernel
@@ -62,14 +71,19 @@
 namespace nvfp4 {
 namespace attn {
 
-constexpr int ATTN_THREADS = 384;
-constexpr int SOFT_WARP0 = 4;
+constexpr int ATTN_THREADS = 512;
+constexpr int ROW_WARP0 = 4;        // warps 4..7: one thread per row
+constexpr int SOFT_WARP0 = 8;       // warps 8..15: softmax
 constexpr int SOFT_THREADS = 256;
+constexpr int STAGE_LD = 36;        // floats of a row of the results' staging: 32 columns, spread over the banks
 constexpr uint64_t ATTN_WAIT_NS = 2000000000ull;
 constexpr uint32_t TMEM_COLS = 512;
-constexpr float P_SHIFT = 8.0f;       // the block's largest probability is near 2^P_SHIFT
-constexpr float REF_UP = 0.75f;       // r moves when the block's largest t leaves [r - REF_DOWN, r + REF_UP]
-constexpr float REF_DOWN = 3.0f;      // 2^(8 + 0.75) < 448
+constexpr float P_SHIFT = 8.0f;       // probabilities are 2^(t - r + P_SHIFT)
+constexpr float REF_SLACK = 1.0f;     // a new r lies this much above the block's largest t
+constexpr float REF_UP = 0.75f;       // 2^(P_SHIFT + REF_UP) < 448
+constexpr float REF_DOWN = 5.0f;
+constexpr float REF_DOWN_THIN = 2.0f; // after a block whose probabilities sum to less than THIN_SUM
+constexpr float THIN_SUM = 64.0f;     // = 2^(P_SHIFT - REF_DOWN_THIN): a block above that edge has it in its largest alone
 constexpr float REF_SPAN = 40.0f;
 
 // What a CTA leaves in the workspace: the state of an item it did not do
@@ -98,6 +112,7 @@ struct AttnParams {
     float *part_o;            // [CTAS][2][part_rows][D]
     float *part_ml;           // [CTAS][2][part_rows][2]: r, sum
     int32_t part_rows;
+    uint32_t group_inv;       // ceil(2^16 / group): row / group = row * group_inv >> 16 for rows below 128
     uint32_t *out_amax;
     uint32_t *status;
 };
@@ -113,20 +128,27 @@ struct AttnShape {
     static constexpr uint32_t S_COL = 256;
 };
 
+constexpr int ITEMS = 4;  // items known ahead
+
 template <int D>
 struct AttnSmem {
+    Item items[ITEMS];
+    uint64_t item_ready[ITEMS], item_done[ITEMS];
     uint64_t full[AttnShape<D>::STAGES], empty[AttnShape<D>::STAGES];
-    uint64_t s_full[2], p_ready[2];
-    uint64_t pv_done, q_ready, o_free, drain;
+    uint64_t s_full[2], p_ready[2], turn_ready[2], pv_done[2];
+    uint64_t q_ready, o_free, stats_ready, drain;
     uint32_t tmem_base;
     volatile int32_t abort_flag;
     WalkStart start;
     int64_t scratch[ATTN_THREADS / 32];
-    float red[2][2][ROW_TILE];     // block maximum of each half row, by block parity
+    float2 red[2][2][ROW_TILE];    // by block parity: each half row's maximum, and its sum of the block before
+    float turn[2][ROW_TILE];       // factor of the accumulated row before this block, by block parity
     float row_scale[ROW_TILE];     // 1 / (power of two of the query row); NaN: the row is not finite
-    float sum[2][ROW_TILE];
+    float sum[2][2][ROW_TILE];     // by item parity: each half row's sum
+    float ref[2][ROW_TILE];        // and the row's reference; -inf: no key seen
     int32_t nan_any[2];            // by item parity
     int32_t nan_key[2][D];         // first key with a NaN value in this dimension
+    alignas(16) float staging[4][32 * STAGE_LD];
 };
 
 template <int D>
@@ -142,9 +164,8 @@ __device__ __forceinline__ void attn_timeout(AttnSmem<D> *sm, uint32_t *status)
     atomicOr(status, kStatusTimeout);
 }
 
-// Order in which K and V blocks of an item of n blocks pass through the ring:
-// K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1).
-__device__ __forceinline__ int ring_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
+// Place of V block j among the K and V blocks of an item of n blocks, which
+// pass through the ring as K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1).
 __device__ __forceinline__ int ring_v(int j, int n) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; }
 
 __device__ __forceinline__ float block_max64(const uint32_t (&v)[64])
@@ -209,14 +230,20 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sm->s_full[i]), 1);
-            mbar_init(smem_u32(&sm->p_ready[i]), SOFT_THREADS / 32);
-            sm->nan_any[i] = 0;
+            mbar_init(smem_u32(&sm->p_ready[i]), SOFT_THREADS / 32 + 4);
+            mbar_init(smem_u32(&sm->turn_ready[i]), 4);
+            mbar_init(smem_u32(&sm->pv_done[i]), 1);
         }
-        mbar_init(smem_u32(&sm->pv_done), 1);
+        for (int i = 0; i < ITEMS; ++i) {
+            mbar_init(smem_u32(&sm->item_ready[i]), 1);
+            mbar_init(smem_u32(&sm->item_done[i]), 4);
+        }
         mbar_init(smem_u32(&sm->q_ready), SOFT_THREADS / 32);
-        mbar_init(smem_u32(&sm->o_free), SOFT_THREADS / 32);
+        mbar_init(smem_u32(&sm->o_free), 4);
+        mbar_init(smem_u32(&sm->stats_ready), SOFT_THREADS / 32);
         mbar_init(smem_u32(&sm->drain), 1);
         sm->abort_flag = 0;
+        sm->nan_any[0] = sm->nan_any[1] = 0;
         fence_mbarrier_init();
         prefetch_tensormap(&tmK);
         prefetch_tensormap(&tmV);
@@ -248,86 +275,83 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
         sm->start.left = 0;
     __syncthreads();
 
-    Walk walk;
-    walk.b = sm->start.b;
-    walk.h = sm->start.h;
-    walk.m = sm->start.m;
-    walk.x = sm->start.x;
-    walk.left = sm->start.left;
-    if (walk.left > 0) {
-        bool ignored = false;
-        walk.q.set(load_seq(p.batch, walk.b, ignored), p.tile_tokens);
-    }
+    // The next item, from warp 2; blocks = 0 at the end or when unwinding.
+    auto take_item = [&](int i, bool &fail) -> Item {
+        Item it;
+        it.blocks = 0;
+        if (!fail && mbar_wait(smem_u32(&sm->item_ready[i % ITEMS]), (i / ITEMS) & 1, ATTN_WAIT_NS))
+            it = sm->items[i % ITEMS];
+        else
+            fail = true;
+        return it;
+    };
 
     if (warp == 0) {
         // ------------------------------------------------------ loads
         const int shift = p.batch.page_shift, page = 1 << shift;
         const int rows = min(page, KEY_BLOCK);        // rows of a box
         const int boxes = KEY_BLOCK / rows;
-        int64_t fills = 0;
-        bool ok = true;
-        for (bool first = true; ok && walk.next(p.batch, p.kv_heads, p.tile_tokens, first); first = false) {
-            const int n = walk.t1 - walk.t0;
-            const int32_t *table = p.batch.table + walk.b * p.batch.table_stride;
-            // page of this lane's box in block t; -1: nothing to load
-            auto page_of = [&](int t) -> int32_t {
-                const int key = t * KEY_BLOCK + lane * rows;
-                return (t < walk.t1 && lane < boxes && key < walk.keys) ? __ldg(table + (key >> shift)) : -1;
-            };
-            auto wanted = [&](int t) -> bool {
-                return t < walk.t1 && lane < boxes && t * KEY_BLOCK + lane * rows < walk.keys;
-            };
-            auto load = [&](const CUtensorMap *map, int row_at, int head_at, int t, int32_t id) -> bool {
-                const int stage = static_cast<int>(fills % A::STAGES);
-                const uint32_t phase = static_cast<uint32_t>(fills / A::STAGES) & 1u;
+        uint32_t fills = 0;
+        bool fail = false, out_of_pool = false;
+        for (int i = 0;; ++i) {
+            const Item it = take_item(i, fail);
+            if (!__all_sync(0xFFFFFFFFu, !fail) || it.blocks == 0)
+                break;
+            const int32_t *table = p.batch.table + it.seq * p.batch.table_stride;
+            const int t1 = it.t0 + it.blocks;
+            // this lane's box of block t has keys, and lies in page:
+            auto wanted = [&](int t) { return t < t1 && lane < boxes && t * KEY_BLOCK + lane * rows < it.keys; };
+            auto page_of = [&](int t) { return wanted(t) ? __ldg(table + ((t * KEY_BLOCK + lane * rows) >> shift)) : 0; };
+            int32_t id = page_of(it.t0), id_next = page_of(it.t0 + 1);  // of blocks t and t + 1
+            int t = it.t0;
+            // K0 K1 V0 K2 V1 .. K(n-1) V(n-2) V(n-1)
+#pragma unroll 1
+            for (int step = 0; step < 2 * it.blocks; ++step) {
+                const bool is_k = step == 0 || ((step & 1) && step < 2 * it.blocks - 1);
+                const int block = is_k && step ? t + 1 : t;
+                const int32_t at = is_k && step ? id_next : id;
+                const uint32_t stage = fills % A::STAGES, phase = (fills / A::STAGES) & 1u;
                 const uint32_t bar = smem_u32(&sm->full[stage]);
-                const int count = __popc(__ballot_sync(0xFFFFFFFFu, wanted(t)));
-                bool good = true;
+                const bool mine = wanted(block);
+                const int count = __popc(__ballot_sync(0xFFFFFFFFu, mine));
                 if (lane == 0) {
-                    good = mbar_wait_bounded(smem_u32(&sm->empty[stage]), phase ^ 1u, ATTN_WAIT_NS);
-                    if (good)
+                    if (mbar_wait(smem_u32(&sm->empty[stage]), phase ^ 1u, ATTN_WAIT_NS))
                         mbar_arrive_expect_tx(bar, static_cast<uint32_t>(count * rows * D));
                     else
-                        attn_timeout(sm, p.status);
+                        fail = true;
                 }
-                good = __shfl_sync(0xFFFFFFFFu, static_cast<int>(good), 0) != 0 && !sm->abort_flag;
-                good = __all_sync(0xFFFFFFFFu, good);
-                if (!good)
-                    return false;
-                if (wanted(t)) {
-                    const int row = (t * KEY_BLOCK + lane * rows) & (page - 1);
+                fail = __any_sync(0xFFFFFFFFu, fail || sm->abort_flag);
+                if (fail)
+                    break;
+                if (mine) {
+                    const int row = (block * KEY_BLOCK + lane * rows) & (page - 1);
                     const uint32_t dst = ring + stage * A::STAGE_BYTES + lane * rows * 128;
-                    const int32_t c1 = row_at == 1 ? row : head_at == 1 ? walk.h : id;
-                    const int32_t c2 = row_at == 2 ? row : head_at == 2 ? walk.h : id;
-                    const int32_t c3 = row_at == 3 ? row : head_at == 3 ? walk.h : id;
+                    const CUtensorMap *map = is_k ? &tmK : &tmV;
+                    const int row_at = is_k ? p.k_row_at : p.v_row_at, head_at = is_k ? p.k_head_at : p.v_head_at;
+                    const int32_t c1 = row_at == 1 ? row : head_at == 1 ? it.head : at;
+                    const int32_t c2 = row_at == 2 ? row : head_at == 2 ? it.head : at;
+                    const int32_t c3 = row_at == 3 ? row : head_at == 3 ? it.head : at;
 #pragma unroll
                     for (int s = 0; s < A::SUBS; ++s)
                         tma_load_4d(dst + s * A::SUB_BYTES, map, s * 128, c1, c2, c3, bar);
                 }
                 ++fills;
-                return true;
-            };
-            int32_t id = page_of(walk.t0), id_next = page_of(walk.t0 + 1);
-            bool out_of_pool = false;
-            ok = load(&tmK, p.k_row_at, p.k_head_at, walk.t0, id);
-            for (int j = 0; ok && j < n; ++j) {
-                const int t = walk.t0 + j;
-                out_of_pool |= wanted(t) && (id < 0 || id >= p.batch.num_pages);
-                const int32_t id_after = page_of(t + 2);
-                if (j + 1 < n)
-                    ok = load(&tmK, p.k_row_at, p.k_head_at, t + 1, id_next);
-                if (ok)
-                    ok = load(&tmV, p.v_row_at, p.v_head_at, t, id);
-                id = id_next;
-                id_next = id_after;
+                if (!is_k) {
+                    out_of_pool |= mine && (id < 0 || id >= p.batch.num_pages);
+                    ++t;
+                    id = id_next;
+                    id_next = page_of(t + 1);
+                }
             }
-            if (out_of_pool)
-                atomicOr(p.status, kStatusBadIndex);
         }
-        // when unwinding, copies in flight land before the shared memory goes away
-        if (lane == 0 && sm->abort_flag)
-            for (int64_t f = max(fills - A::STAGES, int64_t(0)); f < fills; ++f)
-                mbar_wait_bounded(smem_u32(&sm->full[f % A::STAGES]), static_cast<uint32_t>(f / A::STAGES) & 1u, ATTN_WAIT_NS);
+        if (out_of_pool)
+            atomicOr(p.status, kStatusBadIndex);
+        if (fail && lane == 0) {
+            attn_timeout(sm, p.status);
+            // copies in flight land before the shared memory goes away
+            for (uint32_t f = fills > A::STAGES ? fills - A::STAGES : 0; f < fills; ++f)
+                mbar_wait(smem_u32(&sm->full[f % A::STAGES]), (f / A::STAGES) & 1u, ATTN_WAIT_NS);
+        }
     } else if (warp == 1) {
         // ------------------------------------------------------ MMAs
         if (lane == 0) {
@@ -338,249 +362,212 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
             const uint64_t kdesc = smem_desc(ring, 16, 1024, 2);
             // V: rows of 128 bytes; 8-key groups 1024 bytes apart, 128-dimension groups a sub-tile apart
             const uint64_t vdesc = smem_desc(ring, A::SUB_BYTES, 1024, 2);
-            int64_t fill0 = 0;   // ring position of the item's first block
-            int64_t block = 0;   // blocks done
-            int item = 0;
-            bool ok = true;
-            auto wait = [&](uint64_t &bar, uint32_t parity) {
-                if (ok && !mbar_wait_bounded(smem_u32(&bar), parity & 1u, ATTN_WAIT_NS)) {
-                    attn_timeout(sm, p.status);
-                    ok = false;
-                }
-                ok = ok && !sm->abort_flag;
-                return ok;
+            uint32_t uses = 0;   // ring stages consumed
+            uint32_t block = 0;  // blocks of scores begun
+            bool fail = false;
+            auto wait = [&](uint64_t &bar, uint32_t phase) {
+                fail = fail || !mbar_wait(smem_u32(&bar), phase & 1u, ATTN_WAIT_NS);
             };
-            auto scores = [&](int j) {
-                const int64_t f = fill0 + ring_k(j);
-                const int stage = static_cast<int>(f % A::STAGES);
-                if (!wait(sm->full[stage], static_cast<uint32_t>(f / A::STAGES)))
-                    return;
-                tc_fence_after();
-                const uint32_t d = tmem + A::S_COL + ((block + j) & 1) * KEY_BLOCK;
-                const uint64_t kd = kdesc + ((stage * A::STAGE_BYTES) >> 4);
-#pragma unroll
-                for (int i = 0; i < 2 * A::SUBS; ++i)  // high terms' sub-tiles, then the low terms'
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        tc_mma_f8_ss(d, qdesc + ((i * A::SUB_BYTES) >> 4) + 2 * k,
-                                     kd + (((i % A::SUBS) * A::SUB_BYTES) >> 4) + 2 * k, IDESC_S, (i | k) != 0);
-                tc_commit(smem_u32(&sm->empty[stage]));
-                tc_commit(smem_u32(&sm->s_full[(block + j) & 1]));
-            };
-            for (bool first = true; ok && walk.next(p.batch, p.kv_heads, p.tile_tokens, first); first = false, ++item) {
-                const int n = walk.t1 - walk.t0;
-                if (!wait(sm->q_ready, item))
+            for (int i = 0;; ++i) {
+                const Item it = take_item(i, fail);
+                if (fail || it.blocks == 0)
                     break;
-                scores(0);
-                for (int j = 0; ok && j < n; ++j) {
-                    if (j + 1 < n)
-                        scores(j + 1);
-                    if (j == 0 && item > 0 && !wait(sm->o_free, item - 1))
-                        break;
-                    const int64_t bl = block + j, f = fill0 + ring_v(j, n);
-                    const int stage = static_cast<int>(f % A::STAGES);
-                    if (!wait(sm->p_ready[bl & 1], static_cast<uint32_t>(bl >> 1)) ||
-                        !wait(sm->full[stage], static_cast<uint32_t>(f / A::STAGES)))
-                        break;
-                    tc_fence_after();
-                    const uint32_t pb = tmem + A::S_COL + (bl & 1) * KEY_BLOCK;
-                    const uint64_t vd = vdesc + ((stage * A::STAGE_BYTES) >> 4);
+                wait(sm->q_ready, i);
+#pragma unroll 1
+                for (int j = -1; j < it.blocks; ++j) {
+                    if (j + 1 < it.blocks) {  // scores of block j + 1
+                        const uint32_t stage = uses % A::STAGES, buf = block & 1u;
+                        wait(sm->full[stage], uses / A::STAGES);
+                        if (fail)
+                            break;
+                        tc_fence_after();
+                        const uint32_t d = tmem + A::S_COL + buf * KEY_BLOCK;
+                        const uint64_t kd = kdesc + ((stage * A::STAGE_BYTES) >> 4);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        // 32 keys: 8 columns of high terms, 16 columns on their low terms; each half row has its own 64
-                        const uint32_t a = pb + (k >> 1) * 64 + (k & 1) * 8;
-                        const uint64_t b = vd + ((k * 4096) >> 4);
-                        tc_mma_f8_ts(tmem + A::O_COL, a, b, IDESC_O, (j | k) != 0);
-                        tc_mma_f8_ts(tmem + A::O_COL, a + 16, b, IDESC_O, 1);
+                        for (int s = 0; s < 2 * A::SUBS; ++s)  // high terms' sub-tiles, then the low terms'
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                tc_mma_f8_ss(d, qdesc + ((s * A::SUB_BYTES) >> 4) + 2 * k,
+                                             kd + (((s % A::SUBS) * A::SUB_BYTES) >> 4) + 2 * k, IDESC_S, (s | k) != 0);
+                        tc_commit(smem_u32(&sm->empty[stage]));
+                        tc_commit(smem_u32(&sm->s_full[buf]));
+                        ++uses;
+                        ++block;
                     }
-                    tc_commit(smem_u32(&sm->empty[stage]));
-                    tc_commit(smem_u32(&sm->pv_done));
+                    if (j >= 0) {  // values of block j
+                        const uint32_t bl = block - (j + 1 < it.blocks ? 2 : 1);
+                        const uint32_t stage = uses % A::STAGES, buf = bl & 1u;
+                        if (j == 0 && i > 0)
+                            wait(sm->o_free, i - 1);
+                        wait(sm->full[stage], uses / A::STAGES);
+                        wait(sm->p_ready[buf], bl >> 1);
+                        if (fail || sm->abort_flag)
+                            break;
+                        tc_fence_after();
+                        const uint32_t pb = tmem + A::S_COL + buf * KEY_BLOCK;
+                        const uint64_t vd = vdesc + ((stage * A::STAGE_BYTES) >> 4);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            // 32 keys: 8 columns of high terms, 16 columns on their low terms; each half row has its own 64
+                            const uint32_t a = pb + (k >> 1) * 64 + (k & 1) * 8;
+                            const uint64_t b = vd + ((k * 4096) >> 4);
+                            tc_mma_f8_ts(tmem + A::O_COL, a, b, IDESC_O, (j | k) != 0);
+                            tc_mma_f8_ts(tmem + A::O_COL, a + 16, b, IDESC_O, 1);
+                        }
+                        tc_commit(smem_u32(&sm->empty[stage]));
+                        tc_commit(smem_u32(&sm->pv_done[buf]));
+                        ++uses;
+                    }
                 }
-                block += n;
-                fill0 += 2 * n;
+                if (fail || sm->abort_flag) {
+                    fail = true;
+                    break;
+                }
             }
             // every tcgen05 operation of this thread ends before TMEM is freed
             tc_commit(smem_u32(&sm->drain));
-            if (!mbar_wait_bounded(smem_u32(&sm->drain), 0, ATTN_WAIT_NS))
+            if (!mbar_wait(smem_u32(&sm->drain), 0, ATTN_WAIT_NS) || fail)
                 attn_timeout(sm, p.status);
         }
-    } else if (warp >= SOFT_WARP0) {
-        // ------------------------------------------------------ softmax
-        const int quarter = warp & 3, half = (warp - SOFT_WARP0) >> 2, sw = warp - SOFT_WARP0;
-        const int st = tid - SOFT_WARP0 * 32;
-        const int row = quarter * 32 + lane;
-        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-        const float c = p.softmax_scale * ks * 1.4426950408889634f;
+    } else if (warp == 2) {
+        // ------------------------------------------------- items, prefetches
+        Walk walk;
+        walk.b = sm->start.b;
+        walk.h = sm->start.h;
+        walk.m = sm->start.m;
+        walk.x = sm->start.x;
+        walk.left = sm->start.left;
+        if (walk.left > 0) {
+            bool ignored = false;
+            walk.q.set(load_seq(p.batch, walk.b, ignored), p.tile_tokens);
+        }
         PartInfo info;
         info.continues = info.owns = 0;
         info.last = info.token0 = info.rows = info.group0 = info.past0 = info.pad = 0;
-        int64_t block = 0, fill0 = 0;
-        int item = 0;
-        bool fail = false;  // a wait of this thread ran out; the barriers' votes make it everyone's
+        bool fail = false;
+        for (int i = 0;; ++i) {
+            int64_t end_cost = 0;
+            const Item it = walk.next(p.batch, p.kv_heads, p.tile_tokens, p.group, end_cost);
+            const int slot = i % ITEMS;
+            if (i >= ITEMS)
+                fail = !mbar_wait(smem_u32(&sm->item_done[slot]), ((i / ITEMS) - 1) & 1, ATTN_WAIT_NS);
+            fail = __any_sync(0xFFFFFFFFu, fail || sm->abort_flag);
+            if (fail)
+                break;
+            if (lane == 0) {
+                sm->items[slot] = it;
+                mbar_arrive(smem_u32(&sm->item_ready[slot]));
+            }
+            if (it.blocks == 0)
+                break;
+            if (it.part == 1) {
+                info.continues = 1;
+            } else if (it.part == 2) {
+                // the item's last CTA is the one that holds the end of its cost
+                const int64_t all = sm->start.total;
+                info.owns = 1;
+                info.last = static_cast<int>(((all * (cta + 1) / CTAS + end_cost) * CTAS - 1) / all);
+                info.token0 = it.token0;
+                info.rows = it.rows;
+                info.group0 = it.head * p.group;
+                info.past0 = it.past0;
+            }
+#pragma unroll 1
+            for (int which = i > 0 ? 0 : 1; which < 2; ++which) {  // the first item's queries are being read already
+                const HeadRows &x = which ? p.gate : p.q;
+                if (x.data != nullptr && (which == 0 || it.part == 0))
+#pragma unroll 1
+                    for (int k = lane; k < it.rows * (D / 64); k += 32) {
+                        const uint32_t r = k / (D / 64), tk = r * p.group_inv >> 16, g = r - tk * p.group;
+                        const uint16_t *at = x.data + (it.token0 + tk) * x.token_stride +
+                                             (it.head * p.group + g) * x.head_stride + (k % (D / 64)) * 64;
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+                    }
+            }
+        }
+        if (lane == 0) {
+            if (fail)
+                attn_timeout(sm, p.status);
+            p.parts[cta] = info;
+        }
+    } else if (warp >= ROW_WARP0 && warp < SOFT_WARP0) {
+        // ------------------------------------------- rows: rescaling, results
+        const int quarter = warp & 3, rt = tid - ROW_WARP0 * 32, row = rt;
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        float *stage_rows = sm->staging[quarter];
+        uint32_t block = 0, uses = 0;
+        bool fail = false;  // a wait of this thread ran out
         uint32_t amax = 0;
-
-        // Queries of row tile (b, h, m) to shared memory, as two E4M3 terms
-        auto load_queries = [&](const Walk &w) {
-            constexpr int LANES = D / 8, GROUP = 32 / LANES;
-            const int col = (lane % LANES) * 8;
-            const int rows = min(w.q.s.fresh - w.m * p.tile_tokens, p.tile_tokens) * p.group;
-            const int token0 = w.q.s.first + w.m * p.tile_tokens;
-#pragma unroll 4
-            for (int base = sw * GROUP; base < ROW_TILE; base += 8 * GROUP) {
-                if (base >= rows)
-                    break;
-                const int r = base + lane / LANES;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (r < rows) {
-                    const int t = r / p.group, g = r - t * p.group;
-                    v = *reinterpret_cast<const uint4 *>(p.q.data + (token0 + t) * p.q.token_stride +
-                                                         (w.h * p.group + g) * p.q.head_stride + col);
-                }
-                uint2 hi, lo;
-                float unscale;
-                split_query<D>(v, hi, lo, unscale);
-                uint8_t *at = smem + (col >> 7) * A::SUB_BYTES + r * 128 + ((col & 127) ^ ((r & 7) << 4));
-                *reinterpret_cast<uint2 *>(at) = hi;
-                *reinterpret_cast<uint2 *>(at + A::SUBS * A::SUB_BYTES) = lo;
-                if ((lane % LANES) == 0)
-                    sm->row_scale[r] = unscale;
-            }
-            fence_proxy_async_smem();
+        auto wait = [&](uint64_t &bar, uint32_t phase) {
+            fail = fail || !mbar_wait(smem_u32(&bar), phase & 1u, ATTN_WAIT_NS);
             __syncwarp();
-            if (lane == 0)
-                mbar_arrive(smem_u32(&sm->q_ready));
         };
-
-        bool more = walk.next(p.batch, p.kv_heads, p.tile_tokens, true);
-        if (more)
-            load_queries(walk);
-        while (more) {
-            const int n = walk.t1 - walk.t0;
-            const int rows = min(walk.q.s.fresh - walk.m * p.tile_tokens, p.tile_tokens) * p.group;
-            const int past0 = walk.q.past + walk.m * p.tile_tokens;
-            const bool live = row < rows;
-            const bool warp_live = quarter * 32 < rows;
-            const int seen = live ? max(past0 + row / p.group + 1, 0) : 0;  // keys in this row's sight
-            const int seen_first = walk.q.keys_first(walk.m, p.tile_tokens);
-            const int np = item & 1;
-            float f = 0.0f, ref = 0.0f, top = -INFINITY, sum = 0.0f;
-            bool stop = false;
-            named_barrier_any(1, SOFT_THREADS, false);  // row_scale of this item is written
-            if (live) {
-                f = sm->row_scale[row] * c;
-                f = f < 1.17549435e-38f ? 1.17549435e-38f : f;  // keeps (-inf) * f; NaN stays
-            }
-            for (int j = 0; j < n; ++j) {
-                const int t = walk.t0 + j;
-                const int64_t bl = block + j;
-                const int buf = static_cast<int>(bl & 1);
-                if (!mbar_wait_bounded(smem_u32(&sm->s_full[buf]), static_cast<uint32_t>(bl >> 1) & 1u, ATTN_WAIT_NS))
-                    fail = true;
-                __syncwarp();
-                tc_fence_after();
-                const uint32_t scol = tmem + A::S_COL + buf * KEY_BLOCK + half * 64 + lanes;
-                uint32_t v[64];
-                float mine = -INFINITY;
-                if (warp_live) {
-                    tc_ld_32x32b_x64(scol, v);
-                    tc_wait_ld();
-                    const int vis = seen - t * KEY_BLOCK - half * 64;  // keys of this half row in sight
-                    if (__any_sync(0xFFFFFFFFu, vis < 64)) {
+        // The values of block i are in the accumulator.  A wait by parity tells a phase only from its neighbour, so
+        // even and odd blocks have a barrier each: here the scores of block i or i + 1 have been seen, so block
+        // i - 2 is done, and block i + 2 waits for these warps.
+        auto wait_values = [&](uint32_t i) { wait(sm->pv_done[i & 1], i >> 1); };
+        for (int i = 0;; ++i) {
+            const Item it = take_item(i, fail);
+            if (__any_sync(0xFFFFFFFFu, fail))
+                fail = true;
+            if (!fail && it.blocks == 0)
+                break;
+            const int ip = i & 1;
+            const bool live = row < it.rows;
+            // keys in this row's sight
+            const int seen = live ? max(it.past0 + static_cast<int>(row * p.group_inv >> 16) + 1, 0) : 0;
+#pragma unroll 1
+            for (int j = 0; j < it.blocks; ++j, ++block) {
+                const int key0 = (it.t0 + j) * KEY_BLOCK;
+                const int buf = static_cast<int>(block & 1);
+                wait(sm->turn_ready[buf], block >> 1);
+                const float turn = live ? sm->turn[buf][row] : 1.0f;
+                if (__any_sync(0xFFFFFFFFu, turn != 1.0f)) {
+                    wait_values(block - 1);  // not the item's first block
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int k = 0; k < D; k += 32) {
+                        uint32_t o[32];
+                        tc_ld_32x32b_x32(tmem + A::O_COL + k + lanes, o);
+                        tc_wait_ld();
+                        const uint64_t tt = pack2(turn, turn);
 #pragma unroll
-                        for (int i = 0; i < 64; ++i)
-                            v[i] = i < vis ? v[i] : 0xFF800000u;
-                    }
-                    mine = block_max64(v);
-                    sm->red[buf][half][row] = mine;
-                }
-                stop = named_barrier_any(1, SOFT_THREADS, fail);
-                if (stop)
-                    break;
-                if (warp_live) {
-                    const float tm = fmaxf(mine, sm->red[buf][half ^ 1][row]) * f;
-                    float turn = 1.0f;
-                    if (tm > -INFINITY) {
-                        const bool begun = top > -INFINITY;
-                        top = fmaxf(top, tm);
-                        if (!begun) {
-                            ref = tm;
-                        } else if (tm > ref + REF_UP || tm < ref - REF_DOWN) {
-                            const float to = fmaxf(tm, top - REF_SPAN);
-                            turn = exp2_fast(ref - to);
-                            sum *= turn;
-                            ref = to;
+                        for (int e = 0; e < 32; e += 2) {
+                            float a, b;
+                            unpack2(mul2(pack2u(o[e], o[e + 1]), tt), a, b);
+                            o[e] = __float_as_uint(a);
+                            o[e + 1] = __float_as_uint(b);
                         }
+                        tc_st_32x32b_x32(tmem + A::O_COL + k + lanes, o);
                     }
-                    if (__any_sync(0xFFFFFFFFu, turn != 1.0f)) {
-                        // the values of the blocks so far are in the accumulator
-                        if (!mbar_wait_bounded(smem_u32(&sm->pv_done), static_cast<uint32_t>(bl - 1) & 1u, ATTN_WAIT_NS))
-                            fail = true;
-                        __syncwarp();
-                        tc_fence_after();
-#pragma unroll
-                        for (int k = 0; k < D / 64; ++k) {
-                            uint32_t o[32];
-                            const uint32_t oc = tmem + A::O_COL + half * (D / 2) + k * 32 + lanes;
-                            tc_ld_32x32b_x32(oc, o);
-                            tc_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                o[i] = __float_as_uint(__uint_as_float(o[i]) * turn);
-                            tc_st_32x32b_x32(oc, o);
-                        }
-                    }
-                    const float base = P_SHIFT - ref;
-                    float s0 = 0.0f, s1 = 0.0f;
-                    uint32_t hi[16], lo[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float x[4], y[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            x[e] = exp2_fast(fmaf(__uint_as_float(v[4 * i + e]), f, base));
-                            y[e] = __uint_as_float(__float_as_uint(x[e]) & 0xFFF00000u);
-                        }
-                        s0 += x[0] + x[1];
-                        s1 += x[2] + x[3];
-                        hi[i] = f32_to_e4m3x4(y[0], y[1], y[2], y[3]);
-                        lo[i] = f32_to_e4m3x4(x[0] - y[0], x[1] - y[1], x[2] - y[2], x[3] - y[3]);
-                    }
-                    sum += s0 + s1;
-                    tc_st_32x32b_x16(scol, hi);
-                    tc_st_32x32b_x16(scol + 16, lo);
                     tc_wait_st();
                 }
-                if ((t + 1) * KEY_BLOCK > seen_first) {
+                if (key0 + KEY_BLOCK > it.seen_first) {
                     // some row does not see the block to its end
-                    const int64_t fv = fill0 + ring_v(j, n);
-                    const int stage = static_cast<int>(fv % A::STAGES);
-                    if (!mbar_wait_bounded(smem_u32(&sm->full[stage]), static_cast<uint32_t>(fv / A::STAGES) & 1u, ATTN_WAIT_NS))
-                        fail = true;
-                    const int none = walk.keys - t * KEY_BLOCK;         // keys from here on: seen by no row
-                    const int some = seen_first - t * KEY_BLOCK;        // from here on: not by every row
-#pragma unroll 2
-                    for (int i = 0; i < A::SUBS * 4; ++i) {
-                        const int chunk = st + SOFT_THREADS * i;        // 16 bytes: key row, sub-tile
-                        const int key = (chunk >> 3) & 127;
-                        uint4 *at = reinterpret_cast<uint4 *>(smem + A::Q_BYTES + stage * A::STAGE_BYTES) + chunk;
+                    const uint32_t fv = uses + ring_v(j, it.blocks), stage = fv % A::STAGES;
+                    wait(sm->full[stage], fv / A::STAGES);
+                    const int none = it.keys - key0;         // keys from here on: seen by no row
+                    const int some = it.seen_first - key0;   // from here on: not by every row
+#pragma unroll 1
+                    for (int c = rt; c < A::SUBS * 1024; c += 128) {  // 16 bytes: key row, sub-tile
+                        const int key = (c >> 3) & 127;
+                        uint4 *at = reinterpret_cast<uint4 *>(smem + A::Q_BYTES + stage * A::STAGE_BYTES) + c;
                         if (key >= none) {
                             *at = make_uint4(0, 0, 0, 0);
                         } else if (key >= some) {
                             const uint4 x = *at;
-                            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                            uint32_t hit = 0;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                hit |= __vcmpeq4(w[e] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                            const uint32_t hit = __vcmpeq4(x.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(x.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
+                                                 __vcmpeq4(x.z & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(x.w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
                             if (hit) {
-                                const int dim = (chunk >> 10) * 128 + ((chunk ^ key) & 7) * 16;
+                                const int dim = (c >> 10) * 128 + ((c ^ key) & 7) * 16;
                                 uint8_t *bytes = reinterpret_cast<uint8_t *>(at);
+#pragma unroll 1
                                 for (int e = 0; e < 16; ++e)
                                     if ((bytes[e] & 0x7F) == 0x7F) {
-                                        atomicMin(&sm->nan_key[np][dim + e], t * KEY_BLOCK + key);
+                                        atomicMin(&sm->nan_key[ip][dim + e], key0 + key);
                                         bytes[e] = 0;
                                     }
-                                sm->nan_any[np] = 1;
+                                sm->nan_any[ip] = 1;
                             }
                         }
                     }
@@ -591,121 +578,108 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
                 if (lane == 0)
                     mbar_arrive(smem_u32(&sm->p_ready[buf]));
             }
-            if (!stop) {
-                sm->sum[half][row] = sum;
-                stop = named_barrier_any(1, SOFT_THREADS, fail);  // sums and NaN marks are written
-            }
-            if (stop) {
-                fail = true;
-                break;
-            }
-            block += n;
-            fill0 += 2 * n;
-            const Walk done = walk;
-            more = walk.next(p.batch, p.kv_heads, p.tile_tokens, false);
-            if (more)
-                load_queries(walk);  // every score MMA of the item has completed
-            if (!mbar_wait_bounded(smem_u32(&sm->pv_done), static_cast<uint32_t>(block - 1) & 1u, ATTN_WAIT_NS))
-                fail = true;
-            __syncwarp();
-            if (named_barrier_any(1, SOFT_THREADS, fail)) {
-                fail = true;
-                break;
-            }
-            tc_fence_after();
+            uses += 2 * it.blocks;
             // ------------------------------------------------ results
-            const float total = sm->sum[0][row] + sm->sum[1][row];
-            const bool whole = done.t0 == 0 && done.t1 == done.blocks;
-            const int slot = done.t0 == 0 ? 1 : 0;
-            const int token0 = done.q.s.first + done.m * p.tile_tokens;
-            const bool has_nan = sm->nan_any[np] != 0;
-            const int tk = row / p.group, g = row - tk * p.group;
-            const float inv = vs / total;
-            const int64_t prow = (static_cast<int64_t>(cta) * 2 + slot) * p.part_rows + row;
-            if (warp_live) {
+            wait(sm->stats_ready, i);
+            if (it.blocks > 0)
+                wait_values(block - 1);
+            fail = named_barrier_any(2, 128, fail);  // NaN marks are written
+            if (fail)
+                break;
+            tc_fence_after();
+            const float total = sm->sum[ip][0][row] + sm->sum[ip][1][row];
+            const bool whole = it.part == 0, has_nan = sm->nan_any[ip] != 0;
+            const float factor = whole ? vs / total : 1.0f;
+            if (quarter * 32 < it.rows) {
+                // The accumulator has a row per lane; memory wants a row's columns together: 32 columns at a
+                // time pass through shared memory, and 4 lanes take a row's 8 columns each.
+                const int sub = lane >> 2, c8 = (lane & 3) * 8;
+                const int64_t prow0 = (static_cast<int64_t>(cta) * 2 + (it.part == 2 ? 1 : 0)) * p.part_rows;
+                int64_t out_at[4], gate_at[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t r = quarter * 32 + e * 8 + sub, tk = r * p.group_inv >> 16;
+                    const int32_t t = it.token0 + tk, h = it.head * p.group + (r - tk * p.group);
+                    out_at[e] = whole ? t * p.out.token_stride + h * p.out.head_stride + c8 : (prow0 + r) * D + c8;
+                    gate_at[e] = t * p.gate.token_stride + h * p.gate.head_stride + c8;
+                }
 #pragma unroll 1
-                for (int k = 0; k < D / 64; ++k) {
-                    const int col = half * (D / 2) + k * 32;
+                for (int col = 0; col < D; col += 32) {
                     uint32_t o[32];
+                    uint4 gv[4];
+                    if (whole && p.gate.data != nullptr) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (quarter * 32 + e * 8 + sub < it.rows)
+                                gv[e] = *reinterpret_cast<const uint4 *>(p.gate.data + gate_at[e] + col);
+                    }
                     tc_ld_32x32b_x32(tmem + A::O_COL + col + lanes, o);
                     tc_wait_ld();
-                    if (has_nan) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (sm->nan_key[np][col + i] < seen)
-                                o[i] = 0x7FC00000u;
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 y = make_float4(__uint_as_float(o[e]) * factor, __uint_as_float(o[e + 1]) * factor,
+                                                     __uint_as_float(o[e + 2]) * factor, __uint_as_float(o[e + 3]) * factor);
+                        *reinterpret_cast<float4 *>(stage_rows + lane * STAGE_LD + e) = y;
                     }
-                    if (!live) {
-                        // a row of the tile that no token fills
-                    } else if (whole) {
-                        const uint16_t *gp = p.gate.data + (token0 + tk) * p.gate.token_stride +
-                                             (done.h * p.group + g) * p.gate.head_stride + col;
-                        uint16_t *op = const_cast<uint16_t *>(p.out.data) + (token0 + tk) * p.out.token_stride +
-                                       (done.h * p.group + g) * p.out.head_stride + col;
+                    if (live && (seen == 0 || has_nan)) {  // no key in sight, or perhaps a NaN
+#pragma unroll 1
+                        for (int e = 0; e < 32; ++e) {
+                            if (whole && seen == 0)
+                                stage_rows[lane * STAGE_LD + e] = 0.0f;
+                            if (sm->nan_key[ip][col + e] < seen)
+                                stage_rows[lane * STAGE_LD + e] = __uint_as_float(0x7FC00000u);
+                        }
+                    }
+                    __syncwarp();
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
-                            float y[8];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                y[e] = seen > 0 ? __uint_as_float(o[i + e]) * inv : 0.0f;
+                    for (int e = 0; e < 4; ++e) {
+                        const float *src = stage_rows + (e * 8 + sub) * STAGE_LD + c8;
+                        const float4 a = *reinterpret_cast<const float4 *>(src), b = *reinterpret_cast<const float4 *>(src + 4);
+                        if (quarter * 32 + e * 8 + sub >= it.rows)
+                            continue;
+                        if (whole) {
+                            float y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
                             if (p.gate.data != nullptr) {
                                 float gx[8];
-                                unpack8(*reinterpret_cast<const uint4 *>(gp + i), gx);
+                                unpack8(gv[e], gx);
 #pragma unroll
-                                for (int e = 0; e < 8; ++e)
-                                    y[e] = __fdividef(y[e], 1.0f + __expf(-gx[e]));
+                                for (int k = 0; k < 8; ++k)
+                                    y[k] = __fdividef(y[k], 1.0f + __expf(-gx[k]));
                             }
                             const uint4 w = pack8(y);
-                            *reinterpret_cast<uint4 *>(op + i) = w;
-                            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                amax = __vmaxu2(amax, ww[e] & 0x7FFF7FFFu);
+                            *reinterpret_cast<uint4 *>(const_cast<uint16_t *>(p.out.data) + out_at[e] + col) = w;
+                            amax = __vmaxu2(__vmaxu2(amax, w.x & 0x7FFF7FFFu), w.y & 0x7FFF7FFFu);
+                            amax = __vmaxu2(__vmaxu2(amax, w.z & 0x7FFF7FFFu), w.w & 0x7FFF7FFFu);
+                        } else {
+                            float4 *op = reinterpret_cast<float4 *>(p.part_o + out_at[e] + col);
+                            op[0] = a;
+                            op[1] = b;
                         }
-                    } else {
-                        float4 *op = reinterpret_cast<float4 *>(p.part_o + prow * D + col);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            op[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                                __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
                     }
                     __syncwarp();
                 }
-                if (!whole && live && half == 0) {
-                    p.part_ml[prow * 2] = top > -INFINITY ? ref : -INFINITY;
-                    p.part_ml[prow * 2 + 1] = total;
+                if (!whole && live) {
+                    p.part_ml[(prow0 + row) * 2] = sm->ref[ip][row];
+                    p.part_ml[(prow0 + row) * 2 + 1] = total;
                 }
             }
-            if (!whole) {
-                if (slot == 0) {
-                    info.continues = 1;
-                } else {
-                    // the item's last CTA: the one that holds the end of its cost
-                    const int64_t all = sm->start.total;
-                    const int64_t end = all * (cta + 1) / CTAS + done.q.cost(done.m, p.tile_tokens) - done.x;
-                    info.owns = 1;
-                    info.last = static_cast<int>((end * CTAS - 1) / all);
-                    info.token0 = token0;
-                    info.rows = rows;
-                    info.group0 = done.h * p.group;
-                    info.past0 = past0;
-                }
-            }
-            // NaN marks of the next item but one's parity were last read before this item
-            for (int i = st; i < D; i += SOFT_THREADS)
-                sm->nan_key[np ^ 1][i] = INT_MAX;
-            if (st == 0)
-                sm->nan_any[np ^ 1] = 0;
             tc_fence_before();
+            if (has_nan) {  // alike for all 128 threads; the next marks of this parity come behind the next item's barrier
+                named_barrier_any(2, 128, false);
+#pragma unroll 1
+                for (int e = rt; e < D; e += 128)
+                    sm->nan_key[ip][e] = INT_MAX;
+                if (rt == 0)
+                    sm->nan_any[ip] = 0;
+            }
             __syncwarp();
-            if (lane == 0)
+            if (lane == 0) {
                 mbar_arrive(smem_u32(&sm->o_free));
-            ++item;
+                mbar_arrive(smem_u32(&sm->item_done[i % ITEMS]));
+            }
         }
         if (fail && lane == 0)
             attn_timeout(sm, p.status);
-        if (st == 0)
-            p.parts[cta] = info;
         if (p.out_amax != nullptr) {
             amax = max(amax & 0xFFFFu, amax >> 16);
 #pragma unroll
@@ -714,6 +688,169 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
             if (lane == 0 && amax != 0)
                 atomicMax(p.out_amax, amax);
         }
+    } else if (warp >= SOFT_WARP0) {
+        // ------------------------------------------------------ softmax
+        const int quarter = warp & 3, half = (warp - SOFT_WARP0) >> 2, sw = warp - SOFT_WARP0;
+        const int row = quarter * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        const float c = p.softmax_scale * ks * 1.4426950408889634f;
+        uint32_t block = 0;
+        bool fail = false;  // a wait of this thread ran out; the barriers' votes make it everyone's
+        for (int i = 0;; ++i) {
+            const Item it = take_item(i, fail);
+            if (!fail && it.blocks == 0)
+                break;
+            // Queries to shared memory as two E4M3 terms (the score MMAs of the item before have completed): each
+            // warp takes every 8th row, or pair of rows, BATCH loads in flight
+            {
+                constexpr int LANES = D / 8, GROUP = 32 / LANES, BATCH = 4;
+                const int col = (lane % LANES) * 8;
+                const uint16_t *src = p.q.data + it.token0 * p.q.token_stride + it.head * p.group * p.q.head_stride + col;
+                auto load = [&](int r0, uint4 (&v)[BATCH]) {
+#pragma unroll
+                    for (int e = 0; e < BATCH; ++e) {
+                        const uint32_t r = r0 + 8 * GROUP * e + lane / LANES, tk = r * p.group_inv >> 16;
+                        v[e] = make_uint4(0, 0, 0, 0);
+                        if (r < static_cast<uint32_t>(it.rows))
+                            v[e] = *reinterpret_cast<const uint4 *>(src + tk * p.q.token_stride + (r - tk * p.group) * p.q.head_stride);
+                    }
+                };
+                uint4 v[BATCH];
+                load(sw * GROUP, v);
+#pragma unroll 1
+                for (int r0 = sw * GROUP; r0 < it.rows && !fail; r0 += 8 * GROUP * BATCH) {
+                    uint4 next[BATCH];
+                    load(r0 + 8 * GROUP * BATCH, next);
+#pragma unroll
+                    for (int e = 0; e < BATCH; ++e) {
+                        const int r = r0 + 8 * GROUP * e + lane / LANES;
+                        uint2 hi, lo;
+                        float unscale;
+                        split_query<D>(v[e], hi, lo, unscale);
+                        if (r < ROW_TILE) {
+                            uint8_t *at = smem + (col >> 7) * A::SUB_BYTES + r * 128 + ((col & 127) ^ ((r & 7) << 4));
+                            *reinterpret_cast<uint2 *>(at) = hi;
+                            *reinterpret_cast<uint2 *>(at + A::SUBS * A::SUB_BYTES) = lo;
+                            if ((lane % LANES) == 0)
+                                sm->row_scale[r] = unscale;
+                        }
+                        v[e] = next[e];
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_u32(&sm->q_ready));
+            }
+            fail = named_barrier_any(1, SOFT_THREADS, fail);  // row_scale of this item is written
+            if (fail)
+                break;
+            const bool live = row < it.rows, warp_live = quarter * 32 < it.rows;
+            // keys in sight of this half row, from the current block's first; rows that no token fills need no mask
+            int vis = live ? max(it.past0 + static_cast<int>(row * p.group_inv >> 16) + 1, 0) - it.t0 * KEY_BLOCK - half * 64 : INT_MAX;
+            float f = 0.0f, ref = 0.0f, top = -INFINITY;
+            if (live) {
+                f = sm->row_scale[row] * c;
+                f = f < 1.17549435e-38f ? 1.17549435e-38f : f;  // keeps (-inf) * f; NaN stays
+            }
+            const uint64_t ff = pack2(f, f), neg = pack2(-1.0f, -1.0f);
+            uint64_t sum2 = 0;  // two fp32 sums
+            float last = 0.0f;  // sum of the block before
+#pragma unroll 1
+            for (int j = 0; j < it.blocks; ++j, ++block) {
+                const int buf = static_cast<int>(block & 1);
+                fail = fail || !mbar_wait(smem_u32(&sm->s_full[buf]), (block >> 1) & 1u, ATTN_WAIT_NS);
+                __syncwarp();
+                tc_fence_after();
+                const uint32_t scol = tmem + A::S_COL + buf * KEY_BLOCK + half * 64 + lanes;
+                uint32_t v[64];
+                float mine = -INFINITY, turn = 1.0f;
+                if (warp_live) {
+                    tc_ld_32x32b_x64(scol, v);
+                    tc_wait_ld();
+                    if (__any_sync(0xFFFFFFFFu, vis < 64)) {
+#pragma unroll
+                        for (int e = 0; e < 64; ++e)
+                            v[e] = e < vis ? v[e] : 0xFF800000u;
+                    }
+                    mine = block_max64(v);
+                    sm->red[buf][half][row] = make_float2(mine, last);
+                }
+                vis -= live ? KEY_BLOCK : 0;
+                fail = named_barrier_any(1, SOFT_THREADS, fail);
+                if (fail)
+                    break;
+                if (warp_live) {
+                    const float2 other = sm->red[buf][half ^ 1][row];
+                    const float tm = fmaxf(mine, other.x) * f;
+                    if (tm > -INFINITY) {
+                        const bool begun = top > -INFINITY;
+                        top = fmaxf(top, tm);
+                        if (!begun) {
+                            ref = tm + REF_SLACK;
+                        } else if (tm > ref + REF_UP || tm < ref - (last + other.y < THIN_SUM ? REF_DOWN_THIN : REF_DOWN)) {
+                            const float to = fmaxf(tm + REF_SLACK, top - REF_SPAN);
+                            turn = exp2_fast(ref - to);
+                            sum2 = mul2(sum2, pack2(turn, turn));
+                            ref = to;
+                        }
+                    }
+                }
+                if (half == 0) {
+                    sm->turn[buf][row] = turn;
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(smem_u32(&sm->turn_ready[buf]));
+                }
+                if (warp_live) {
+                    const uint64_t bb = pack2(P_SHIFT - ref, P_SHIFT - ref);
+                    uint64_t sum_a = 0, sum_b = 0;
+                    uint32_t hi[16], lo[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        uint64_t x[2], y[2], z[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float a, b;
+                            unpack2(fma2(pack2u(v[4 * k + 2 * e], v[4 * k + 2 * e + 1]), ff, bb), a, b);
+                            a = exp2_fast(a);
+                            b = exp2_fast(b);
+                            x[e] = pack2(a, b);
+                            y[e] = pack2u(__float_as_uint(a) & 0xFFF00000u, __float_as_uint(b) & 0xFFF00000u);
+                            z[e] = fma2(y[e], neg, x[e]);
+                        }
+                        sum_a = add2(sum_a, x[0]);
+                        sum_b = add2(sum_b, x[1]);
+                        hi[k] = e4m3x4_of(y[0], y[1]);
+                        lo[k] = e4m3x4_of(z[0], z[1]);
+                    }
+                    sum_a = add2(sum_a, sum_b);
+                    sum2 = add2(sum2, sum_a);
+                    float sa, sb;
+                    unpack2(sum_a, sa, sb);
+                    last = sa + sb;
+                    tc_st_32x32b_x16(scol, hi);
+                    tc_st_32x32b_x16(scol + 16, lo);
+                    tc_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_u32(&sm->p_ready[buf]));
+            }
+            if (fail)
+                break;
+            float sa, sb;
+            unpack2(sum2, sa, sb);
+            sm->sum[i & 1][half][row] = sa + sb;
+            if (half == 0)
+                sm->ref[i & 1][row] = top > -INFINITY ? ref : -INFINITY;
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_u32(&sm->stats_ready));
+        }
+        if (fail && lane == 0)
+            attn_timeout(sm, p.status);
     }
 
     tc_fence_before();

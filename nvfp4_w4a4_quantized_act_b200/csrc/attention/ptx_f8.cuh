@@ -48,6 +48,38 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
+// mbar_wait_bounded of ptx_sm100.cuh for kernels with many waiting warps: each
+// try suspends the thread for up to `kSuspendNs` instead of polling, so that
+// waiting warps leave the issue slots to the working ones.
+constexpr uint32_t kSuspendNs = 50000;
+
+__device__ __forceinline__ bool mbar_try_wait_suspended(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kSuspendNs)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __noinline__ bool mbar_wait_suspended(uint32_t bar, uint32_t parity, uint64_t limit_ns)
+{
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait_suspended(bar, parity))
+        if (global_timer_ns() - t0 > limit_ns)
+            return false;
+    return true;
+}
+
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns)
+{
+    return mbar_try_wait(bar, parity) || mbar_wait_suspended(bar, parity, limit_ns);
+}
+
 // Barrier over `count` threads that returns, to all of them alike, whether
 // any of them passed a true predicate.
 __device__ __forceinline__ bool named_barrier_any(uint32_t id, uint32_t count, bool mine)
@@ -75,6 +107,47 @@ __device__ __forceinline__ uint32_t f32_to_e4m3x4(float a, float b, float c, flo
         : "=r"(r)
         : "f"(a), "f"(b), "f"(c), "f"(d));
     return r;
+}
+
+// Two fp32 values in a register pair, and the packed arithmetic on them.
+__device__ __forceinline__ uint64_t pack2u(uint32_t lo, uint32_t hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ __forceinline__ uint64_t pack2(float lo, float hi)
+{
+    return pack2u(__float_as_uint(lo), __float_as_uint(hi));
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &lo, float &hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t e4m3x4_of(uint64_t ab, uint64_t cd)
+{
+    float a, b, c, d;
+    unpack2(ab, a, b);
+    unpack2(cd, c, d);
+    return f32_to_e4m3x4(a, b, c, d);
 }
 
 // 2^x, flushing to zero; relative error below 2^-22.

@@ -121,8 +121,8 @@ def attention_ref(cache, b, q, gate, softmax_scale):
         both shift a score by e_s, every weight by a factor within e^(+-e_s),
         the quotient by 2 e_s of sum p |v|;
       each probability as two E4M3 terms of 8 bits together (2^-8 of it), and
-        never finer than 2^-9 where the largest of the 128 keys beside it is
-        at least 32: 2^-14 of that largest;
+        never finer than 2^-9 in units in which the 128 keys of its block, or
+        of the block before, sum to 64 at least: 2^-15 of those sums;
       32-bit sums: 2^-18 of the sums of magnitudes."""
     new, n = cache.seqs[b]
     Hq = q.shape[1]
@@ -151,8 +151,9 @@ def attention_ref(cache, b, q, gate, softmax_scale):
         a = p @ vs.abs() / l
         # a NaN value in sight makes its dimension NaN
         o = torch.where((seen.double() @ torch.isnan(vv).double()) > 0, math.nan, o)
-        tile = torch.nn.functional.pad(p, (0, pad)).view(new, -1, 128).amax(-1)
-        fine = tile.repeat_interleave(128, 1)[:, :n] * seen @ vs.abs() / l * 2.0 ** -14
+        block = torch.nn.functional.pad(p, (0, pad)).view(new, -1, 128).sum(-1)
+        block[:, 1:] += block[:, :-1].clone()
+        fine = block.repeat_interleave(128, 1)[:, :n] * seen @ vs.abs() / l * 2.0 ** -15
         big, kabs = qq.abs().amax(1, keepdim=True), torch.nan_to_num(kk).abs()
         e_s = (f * (big * 2.0 ** -17 * kabs.sum(1)[None] + 2.0 ** -18 * (qq.abs() @ kabs.t()))) * seen
         e = 2 * e_s.amax(1, keepdim=True) + 2.0 ** -8 + 2.0 ** -18
@@ -179,10 +180,17 @@ def check(got, ref, tol, what=""):
 
 
 def check_attention(cache, q, gate, out, softmax_scale, before=None, only=None):
+    """Every sequence's rows within their bounds; and all together within 2^-7
+    in the 2-norm, twice what rounding to bf16 alone may be off: the bounds of
+    single values allow for errors that all point one way."""
+    off = size = 0.0
     for b, (new, _) in enumerate(cache.seqs):
         if new and (only is None or b in only):
             rows = slice(cache.ends[b], cache.ends[b + 1])
             ref, tol = attention_ref(cache, b, q[rows], None if gate is None else gate[rows], softmax_scale)
             check(out[rows], ref, tol, f"sequence {b} {cache.seqs[b]}")
+            off += float(torch.nan_to_num(out[rows].double() - ref).square().sum())
+            size += float(torch.nan_to_num(ref).square().sum())
+    assert off <= 2.0 ** -14 * size, f"2-norm of the error {(off / size) ** 0.5:.2g} of the result's"
     if before is not None:  # rows of no sequence keep what they held
         assert torch.equal(out[cache.total:].view(torch.int16), before[cache.total:].view(torch.int16))
