@@ -2,8 +2,8 @@
 //
 // An item is a tile of query rows of one sequence and key head: up to
 // 128 / group tokens with all `group` query heads of the key head, so every
-// key block loaded serves all of them.  An item costs its keys plus one block
-// of 128 (loading the queries, writing the result).  The items of the batch,
+// key block loaded serves all of them.  An item costs its keys plus ITEM_COST
+// (loading the queries, filling the pipeline, writing the result).  The items of the batch,
 // ordered by sequence, key head and row tile, form one line of cost; CTA c of
 // n takes the c-th n-th of it, whatever the mix of long and short sequences,
 // prompts and single tokens.  A boundary inside an item falls between two of
@@ -21,6 +21,7 @@ namespace attn {
 
 constexpr int KEY_BLOCK = 128;
 constexpr int ROW_TILE = 128;
+constexpr int ITEM_COST = 512;
 constexpr int CTAS = 148;   // one per SM; results do not depend on the device's own count
 
 struct SeqItems {
@@ -40,11 +41,11 @@ struct SeqItems {
     // Cost of row tile m, and of all row tiles before m.
     __device__ __forceinline__ int64_t cost(int m, int tile_tokens) const
     {
-        return KEY_BLOCK + max(static_cast<int64_t>(past) + static_cast<int64_t>(tile_tokens) * (m + 1), int64_t(0));
+        return ITEM_COST + max(static_cast<int64_t>(past) + static_cast<int64_t>(tile_tokens) * (m + 1), int64_t(0));
     }
     __device__ __forceinline__ int64_t before(int m, int tile_tokens) const
     {
-        int64_t sum = static_cast<int64_t>(KEY_BLOCK) * m;
+        int64_t sum = static_cast<int64_t>(ITEM_COST) * m;
         if (m > m0) {
             const int64_t n = m - m0;
             sum += n * past + tile_tokens * (n * m0 + n * (n + 1) / 2);

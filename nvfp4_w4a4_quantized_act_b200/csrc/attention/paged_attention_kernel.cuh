@@ -16,15 +16,16 @@
 //   largest, off by at most 2^-17 of the largest below.
 //   Probabilities: 2^(t - r + 8); high keeps 4 significant bits by
 //   truncation, low = E4M3(p - high): 8 bits together, as bf16 would keep, but
-//   no finer than 2^-9.  So the reference r has to keep a block's
-//   probabilities up: it follows the blocks of 128 keys both ways, not only
-//   up as a running maximum would (after a key far above the rest, a sink,
-//   the others would lose their bits).  A block's largest may lie 0.75 above r
-//   and 5 below it, or 2 below it where the block before had a sum under 64:
-//   then a block's sum or its neighbour's is at least 64, and 128 errors of
-//   2^-9 stay under 2^-8 of it.  When r moves (to 1 above the block's largest)
-//   the accumulated row is rescaled by the exact difference; the wide window
-//   makes that rare, the bound on the sum keeps it safe.  r never falls more
+//   no finer than 2^-9.  So the reference r has to keep the probabilities up:
+//   it follows the blocks of 128 keys both ways, not only up as a running
+//   maximum would (after a key far above the rest, a sink, the others would
+//   lose their bits).  r moves up when a block's largest t is more than 0.75
+//   above it (2^8.75 < 448), and down when it is more than 3 below while the
+//   sum so far is under 32 for each block: so the 128 errors of at most 2^-9
+//   of a block stay under 2^-7 of its share of the sum, in the worst case of
+//   keys that all round the same way.  A new r lies 1.5 above (3 above on the
+//   way down) the block's largest, so that the blocks around it fit; the
+//   accumulated row is rescaled by the exact difference.  r never falls more
 //   than 40 below the largest t so far, under which nothing counts in 32 bits.
 //
 // One CTA per SM; query tile of 128 rows (tokens x query heads of one key
@@ -61,6 +62,7 @@
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "attention_schedule.cuh"
 #include "head_rows_kernels.cuh"
@@ -79,11 +81,11 @@ constexpr int STAGE_LD = 36;        // floats of a row of the results' staging: 
 constexpr uint64_t ATTN_WAIT_NS = 2000000000ull;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr float P_SHIFT = 8.0f;       // probabilities are 2^(t - r + P_SHIFT)
-constexpr float REF_SLACK = 1.0f;     // a new r lies this much above the block's largest t
 constexpr float REF_UP = 0.75f;       // 2^(P_SHIFT + REF_UP) < 448
-constexpr float REF_DOWN = 5.0f;
-constexpr float REF_DOWN_THIN = 2.0f; // after a block whose probabilities sum to less than THIN_SUM
-constexpr float THIN_SUM = 64.0f;     // = 2^(P_SHIFT - REF_DOWN_THIN): a block above that edge has it in its largest alone
+constexpr float REF_DOWN = 3.0f;
+constexpr float BLOCK_SUM = 32.0f;    // 2^(P_SHIFT - REF_DOWN): a block above that edge has it in its largest alone
+constexpr float SLACK_UP = 1.5f;      // how far a new r lies above the block's largest t
+constexpr float SLACK_DOWN = 3.0f;
 constexpr float REF_SPAN = 40.0f;
 
 // What a CTA leaves in the workspace: the state of an item it did not do
@@ -141,7 +143,7 @@ struct AttnSmem {
     volatile int32_t abort_flag;
     WalkStart start;
     int64_t scratch[ATTN_THREADS / 32];
-    float2 red[2][2][ROW_TILE];    // by block parity: each half row's maximum, and its sum of the block before
+    float2 red[2][2][ROW_TILE];    // by block parity: each half row's maximum, and its sum so far
     float turn[2][ROW_TILE];       // factor of the accumulated row before this block, by block parity
     float row_scale[ROW_TILE];     // 1 / (power of two of the query row); NaN: the row is not finite
     float sum[2][2][ROW_TILE];     // by item parity: each half row's sum
@@ -170,13 +172,16 @@ __device__ __forceinline__ int ring_v(int j, int n) { return j == n - 1 ? 2 * n 
 
 __device__ __forceinline__ float block_max64(const uint32_t (&v)[64])
 {
-    float a = fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1])), b = fmaxf(__uint_as_float(v[2]), __uint_as_float(v[3]));
+    float m[4];
 #pragma unroll
-    for (int i = 4; i < 64; i += 4) {
-        a = fmaxf(fmaxf(a, __uint_as_float(v[i])), __uint_as_float(v[i + 1]));
-        b = fmaxf(fmaxf(b, __uint_as_float(v[i + 2])), __uint_as_float(v[i + 3]));
+    for (int k = 0; k < 4; ++k) {
+        m[k] = __uint_as_float(v[k]);
+#pragma unroll
+        for (int i = k + 4; i + 4 < 64; i += 8)
+            m[k] = max3(m[k], __uint_as_float(v[i]), __uint_as_float(v[i + 4]));
+        m[k] = fmaxf(m[k], __uint_as_float(v[60 + k]));
     }
-    return fmaxf(a, b);
+    return max3(m[0], m[1], fmaxf(m[2], m[3]));
 }
 
 // One bf16 query row (8 elements of each lane, D / 8 lanes) as two E4M3 terms.
@@ -189,25 +194,28 @@ __device__ __forceinline__ void split_query(const uint4 &v, uint2 &hi, uint2 &lo
     for (int i = 0; i < 4; ++i)
         mag = __vmaxu2(mag, w[i] & 0x7FFF7FFFu);
     mag = max(mag & 0xFFFFu, mag >> 16);
+    if (D == 256) {
+        mag = __reduce_max_sync(0xFFFFFFFFu, mag);
+    } else {
 #pragma unroll
-    for (int o = D / 16; o > 0; o >>= 1)
-        mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, o));
+        for (int o = D / 16; o > 0; o >>= 1)
+            mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, o));
+    }
     // exponent field e of the largest: scale by 2^(134 - e); at most 2^127
     const int e = static_cast<int>(mag >> 7);
     const int up = min(134 - e, 127);
     const float scale = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
     unscale = e == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
-    uint32_t hw[2], lw[2];
+    // a scaled value is exact in f16 (8 bits; below 2^-14 it is far under the low term's step), and so is x - high
+    uint32_t h[4], l[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float a = __uint_as_float(w[2 * i] << 16) * scale, b = __uint_as_float(w[2 * i] & 0xFFFF0000u) * scale;
-        const float c = __uint_as_float(w[2 * i + 1] << 16) * scale, d = __uint_as_float(w[2 * i + 1] & 0xFFFF0000u) * scale;
-        hw[i] = f32_to_e4m3x4(a, b, c, d);
-        lw[i] = f32_to_e4m3x4(a - e4m3_to_f32(hw[i]), b - e4m3_to_f32(hw[i] >> 8), c - e4m3_to_f32(hw[i] >> 16),
-                              d - e4m3_to_f32(hw[i] >> 24));
+    for (int i = 0; i < 4; ++i) {
+        const __half2 x = __floats2half2_rn(__uint_as_float(w[i] << 16) * scale, __uint_as_float(w[i] & 0xFFFF0000u) * scale);
+        h[i] = f16x2_to_e4m3x2(x);
+        l[i] = f16x2_to_e4m3x2(__hsub2(x, e4m3x2_to_f16x2(h[i])));
     }
-    hi = make_uint2(hw[0], hw[1]);
-    lo = make_uint2(lw[0], lw[1]);
+    hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+    lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
 }
 
 template <int D>
@@ -525,20 +533,20 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
                 if (__any_sync(0xFFFFFFFFu, turn != 1.0f)) {
                     wait_values(block - 1);  // not the item's first block
                     tc_fence_after();
+                    const uint64_t tt = pack2(turn, turn);
 #pragma unroll 1
-                    for (int k = 0; k < D; k += 32) {
-                        uint32_t o[32];
-                        tc_ld_32x32b_x32(tmem + A::O_COL + k + lanes, o);
+                    for (int k = 0; k < D; k += 64) {
+                        uint32_t o[64];
+                        tc_ld_32x32b_x64(tmem + A::O_COL + k + lanes, o);
                         tc_wait_ld();
-                        const uint64_t tt = pack2(turn, turn);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
+                        for (int e = 0; e < 64; e += 2) {
                             float a, b;
                             unpack2(mul2(pack2u(o[e], o[e + 1]), tt), a, b);
                             o[e] = __float_as_uint(a);
                             o[e + 1] = __float_as_uint(b);
                         }
-                        tc_st_32x32b_x32(tmem + A::O_COL + k + lanes, o);
+                        tc_st_32x32b_x64(tmem + A::O_COL + k + lanes, o);
                     }
                     tc_wait_st();
                 }
@@ -755,7 +763,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
             }
             const uint64_t ff = pack2(f, f), neg = pack2(-1.0f, -1.0f);
             uint64_t sum2 = 0;  // two fp32 sums
-            float last = 0.0f;  // sum of the block before
+            float so_far = 0.0f;
 #pragma unroll 1
             for (int j = 0; j < it.blocks; ++j, ++block) {
                 const int buf = static_cast<int>(block & 1);
@@ -774,7 +782,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
                             v[e] = e < vis ? v[e] : 0xFF800000u;
                     }
                     mine = block_max64(v);
-                    sm->red[buf][half][row] = make_float2(mine, last);
+                    sm->red[buf][half][row] = make_float2(mine, so_far);
                 }
                 vis -= live ? KEY_BLOCK : 0;
                 fail = named_barrier_any(1, SOFT_THREADS, fail);
@@ -787,12 +795,15 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
                         const bool begun = top > -INFINITY;
                         top = fmaxf(top, tm);
                         if (!begun) {
-                            ref = tm + REF_SLACK;
-                        } else if (tm > ref + REF_UP || tm < ref - (last + other.y < THIN_SUM ? REF_DOWN_THIN : REF_DOWN)) {
-                            const float to = fmaxf(tm + REF_SLACK, top - REF_SPAN);
-                            turn = exp2_fast(ref - to);
-                            sum2 = mul2(sum2, pack2(turn, turn));
-                            ref = to;
+                            ref = tm + SLACK_UP;
+                        } else {
+                            const bool up = tm > ref + REF_UP;
+                            if (up || (tm < ref - REF_DOWN && so_far + other.y < BLOCK_SUM * static_cast<float>(j))) {
+                                const float to = fmaxf(tm + (up ? SLACK_UP : SLACK_DOWN), top - REF_SPAN);
+                                turn = exp2_fast(ref - to);
+                                sum2 = mul2(sum2, pack2(turn, turn));
+                                ref = to;
+                            }
                         }
                     }
                 }
@@ -804,7 +815,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
                 }
                 if (warp_live) {
                     const uint64_t bb = pack2(P_SHIFT - ref, P_SHIFT - ref);
-                    uint64_t sum_a = 0, sum_b = 0;
+                    uint64_t sum_b = 0;
                     uint32_t hi[16], lo[16];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
@@ -819,16 +830,15 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
                             y[e] = pack2u(__float_as_uint(a) & 0xFFF00000u, __float_as_uint(b) & 0xFFF00000u);
                             z[e] = fma2(y[e], neg, x[e]);
                         }
-                        sum_a = add2(sum_a, x[0]);
+                        sum2 = add2(sum2, x[0]);
                         sum_b = add2(sum_b, x[1]);
                         hi[k] = e4m3x4_of(y[0], y[1]);
                         lo[k] = e4m3x4_of(z[0], z[1]);
                     }
-                    sum_a = add2(sum_a, sum_b);
-                    sum2 = add2(sum2, sum_a);
+                    sum2 = add2(sum2, sum_b);
                     float sa, sb;
-                    unpack2(sum_a, sa, sb);
-                    last = sa + sb;
+                    unpack2(sum2, sa, sb);
+                    so_far = sa + sb;
                     tc_st_32x32b_x16(scol, hi);
                     tc_st_32x32b_x16(scol + 16, lo);
                     tc_wait_st();
@@ -840,9 +850,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
             }
             if (fail)
                 break;
-            float sa, sb;
-            unpack2(sum2, sa, sb);
-            sm->sum[i & 1][half][row] = sa + sb;
+            sm->sum[i & 1][half][row] = so_far;
             if (half == 0)
                 sm->ref[i & 1][row] = top > -INFINITY ? ref : -INFINITY;
             __syncwarp();

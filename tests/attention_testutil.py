@@ -122,7 +122,8 @@ def attention_ref(cache, b, q, gate, softmax_scale):
         the quotient by 2 e_s of sum p |v|;
       each probability as two E4M3 terms of 8 bits together (2^-8 of it), and
         never finer than 2^-9 in units in which the 128 keys of its block, or
-        of the block before, sum to 64 at least: 2^-15 of those sums;
+        the blocks before on average, sum to 32 at least: 2^-14 of the largest
+        sum of a block so far;
       32-bit sums: 2^-18 of the sums of magnitudes."""
     new, n = cache.seqs[b]
     Hq = q.shape[1]
@@ -152,8 +153,7 @@ def attention_ref(cache, b, q, gate, softmax_scale):
         # a NaN value in sight makes its dimension NaN
         o = torch.where((seen.double() @ torch.isnan(vv).double()) > 0, math.nan, o)
         block = torch.nn.functional.pad(p, (0, pad)).view(new, -1, 128).sum(-1)
-        block[:, 1:] += block[:, :-1].clone()
-        fine = block.repeat_interleave(128, 1)[:, :n] * seen @ vs.abs() / l * 2.0 ** -15
+        fine = block.cummax(1)[0].repeat_interleave(128, 1)[:, :n] * seen @ vs.abs() / l * 2.0 ** -14
         big, kabs = qq.abs().amax(1, keepdim=True), torch.nan_to_num(kk).abs()
         e_s = (f * (big * 2.0 ** -17 * kabs.sum(1)[None] + 2.0 ** -18 * (qq.abs() @ kabs.t()))) * seen
         e = 2 * e_s.amax(1, keepdim=True) + 2.0 ** -8 + 2.0 ** -18
