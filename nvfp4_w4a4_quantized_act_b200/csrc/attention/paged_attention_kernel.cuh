@@ -137,7 +137,8 @@ struct AttnSmem {
     Item items[ITEMS];
     uint64_t item_ready[ITEMS], item_done[ITEMS];
     uint64_t full[AttnShape<D>::STAGES], empty[AttnShape<D>::STAGES];
-    uint64_t s_full[2], p_ready[2], turn_ready[2], pv_done[2];
+    uint64_t s_full[2], turn_ready[2], pv_done[2];
+    uint64_t p_ready[2], p_rest[2];  // probabilities of the first 32 keys of each half row, of the others
     uint64_t q_ready, o_free, stats_ready, drain;
     uint32_t tmem_base;
     volatile int32_t abort_flag;
@@ -228,7 +229,8 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(attn_smem_raw) + 1023) & ~uintptr_t(1023));
     AttnSmem<D> *sm = reinterpret_cast<AttnSmem<D> *>(smem + A::Q_BYTES + A::STAGES * A::STAGE_BYTES);
     const uint32_t q_smem = smem_u32(smem), ring = q_smem + A::Q_BYTES;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // uniform to the compiler too
     const int cta = blockIdx.x;
 
     if (tid == 0) {
@@ -239,6 +241,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sm->s_full[i]), 1);
             mbar_init(smem_u32(&sm->p_ready[i]), SOFT_THREADS / 32 + 4);
+            mbar_init(smem_u32(&sm->p_rest[i]), SOFT_THREADS / 32);
             mbar_init(smem_u32(&sm->turn_ready[i]), 4);
             mbar_init(smem_u32(&sm->pv_done[i]), 1);
         }
@@ -362,7 +365,9 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
         }
     } else if (warp == 1) {
         // ------------------------------------------------------ MMAs
-        if (lane == 0) {
+        // One lane, elected: with the election the compiler keeps descriptors and loop state in uniform registers, and
+        // an MMA takes 10 instructions instead of 24.  This thread's own instructions are what bounds the MMA rate.
+        if (elect_one()) {
             // E4M3 x E4M3 -> fp32, M = 128; scores: N = 128 keys, K-major; values: N = D, V's dimensions contiguous
             constexpr uint32_t IDESC_S = (1u << 4) | (uint32_t(KEY_BLOCK >> 3) << 17) | (uint32_t(ROW_TILE >> 4) << 24);
             constexpr uint32_t IDESC_O = (1u << 4) | (1u << 16) | (uint32_t(D >> 3) << 17) | (uint32_t(ROW_TILE >> 4) << 24);
@@ -381,50 +386,65 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
                 if (fail || it.blocks == 0)
                     break;
                 wait(sm->q_ready, i);
+                wait(sm->full[uses % A::STAGES], uses / A::STAGES);
+                // The tensor pipe queues an MMA or two; a wait costs some 70 cycles even when its phase is over.  So
+                // each wait comes ahead of the last MMAs before the ones that need it, not between the products.
 #pragma unroll 1
-                for (int j = -1; j < it.blocks; ++j) {
-                    if (j + 1 < it.blocks) {  // scores of block j + 1
-                        const uint32_t stage = uses % A::STAGES, buf = block & 1u;
-                        wait(sm->full[stage], uses / A::STAGES);
-                        if (fail)
-                            break;
+                for (int j = -1; j < it.blocks && !fail; ++j) {
+                    const bool more = j + 1 < it.blocks;
+                    const uint32_t ks = uses % A::STAGES, sbuf = block & 1u;           // K block j + 1
+                    const uint32_t vu = uses + (more ? 1 : 0), vst = vu % A::STAGES;   // V block j
+                    const uint32_t bl = block - 1, buf = bl & 1u;                      // scores of block j
+                    if (more) {
                         tc_fence_after();
-                        const uint32_t d = tmem + A::S_COL + buf * KEY_BLOCK;
-                        const uint64_t kd = kdesc + ((stage * A::STAGE_BYTES) >> 4);
+                        const uint32_t d = tmem + A::S_COL + sbuf * KEY_BLOCK;
+                        const uint64_t kd = kdesc + ((ks * A::STAGE_BYTES) >> 4);
 #pragma unroll
-                        for (int s = 0; s < 2 * A::SUBS; ++s)  // high terms' sub-tiles, then the low terms'
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                tc_mma_f8_ss(d, qdesc + ((s * A::SUB_BYTES) >> 4) + 2 * k,
-                                             kd + (((s % A::SUBS) * A::SUB_BYTES) >> 4) + 2 * k, IDESC_S, (s | k) != 0);
-                        tc_commit(smem_u32(&sm->empty[stage]));
-                        tc_commit(smem_u32(&sm->s_full[buf]));
+                        for (int m = 0; m < 8 * A::SUBS; ++m) {  // high terms' sub-tiles, then the low terms'
+                            const int s = m >> 2, k = m & 3;
+                            if (m == 8 * A::SUBS - 3 && j >= 0) {
+                                if (j == 0 && i > 0)
+                                    wait(sm->o_free, i - 1);
+                                wait(sm->full[vst], vu / A::STAGES);
+                                wait(sm->p_ready[buf], bl >> 1);
+                            }
+                            tc_mma_f8_ss(d, qdesc + ((s * A::SUB_BYTES) >> 4) + 2 * k,
+                                         kd + (((s % A::SUBS) * A::SUB_BYTES) >> 4) + 2 * k, IDESC_S, m != 0);
+                        }
+                        tc_commit(smem_u32(&sm->empty[ks]));
+                        tc_commit(smem_u32(&sm->s_full[sbuf]));
                         ++uses;
                         ++block;
-                    }
-                    if (j >= 0) {  // values of block j
-                        const uint32_t bl = block - (j + 1 < it.blocks ? 2 : 1);
-                        const uint32_t stage = uses % A::STAGES, buf = bl & 1u;
+                    } else {
                         if (j == 0 && i > 0)
                             wait(sm->o_free, i - 1);
-                        wait(sm->full[stage], uses / A::STAGES);
+                        wait(sm->full[vst], vu / A::STAGES);
                         wait(sm->p_ready[buf], bl >> 1);
-                        if (fail || sm->abort_flag)
-                            break;
+                    }
+                    if (j >= 0) {
                         tc_fence_after();
                         const uint32_t pb = tmem + A::S_COL + buf * KEY_BLOCK;
-                        const uint64_t vd = vdesc + ((stage * A::STAGE_BYTES) >> 4);
+                        const uint64_t vd = vdesc + ((vst * A::STAGE_BYTES) >> 4);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            // 32 keys: 8 columns of high terms, 16 columns on their low terms; each half row has its own 64
-                            const uint32_t a = pb + (k >> 1) * 64 + (k & 1) * 8;
-                            const uint64_t b = vd + ((k * 4096) >> 4);
+                            // 32 keys of a half row: 8 columns of high terms, 16 columns on their low terms; each half
+                            // has its own 64 columns.  The first 32 keys of both come first.
+                            const uint32_t a = pb + (k & 1) * 64 + (k >> 1) * 8;
+                            const uint64_t b = vd + ((((k & 1) * 2 + (k >> 1)) * 4096) >> 4);
+                            if (k == 2) {
+                                wait(sm->p_rest[buf], bl >> 1);
+                                tc_fence_after();
+                            }
+                            if (k == 3 && j + 2 < it.blocks)
+                                wait(sm->full[(uses + 1) % A::STAGES], (uses + 1) / A::STAGES);
                             tc_mma_f8_ts(tmem + A::O_COL, a, b, IDESC_O, (j | k) != 0);
                             tc_mma_f8_ts(tmem + A::O_COL, a + 16, b, IDESC_O, 1);
                         }
-                        tc_commit(smem_u32(&sm->empty[stage]));
+                        tc_commit(smem_u32(&sm->empty[vst]));
                         tc_commit(smem_u32(&sm->pv_done[buf]));
                         ++uses;
+                    } else if (1 < it.blocks) {
+                        wait(sm->full[uses % A::STAGES], uses / A::STAGES);
                     }
                 }
                 if (fail || sm->abort_flag) {
@@ -591,7 +611,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
             wait(sm->stats_ready, i);
             if (it.blocks > 0)
                 wait_values(block - 1);
-            fail = named_barrier_any(2, 128, fail);  // NaN marks are written
+            fail = named_barrier_any(6, 128, fail);  // NaN marks are written
             if (fail)
                 break;
             tc_fence_after();
@@ -673,7 +693,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
             }
             tc_fence_before();
             if (has_nan) {  // alike for all 128 threads; the next marks of this parity come behind the next item's barrier
-                named_barrier_any(2, 128, false);
+                named_barrier_any(6, 128, false);
 #pragma unroll 1
                 for (int e = rt; e < D; e += 128)
                     sm->nan_key[ip][e] = INT_MAX;
@@ -703,7 +723,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         const float c = p.softmax_scale * ks * 1.4426950408889634f;
         uint32_t block = 0;
-        bool fail = false;  // a wait of this thread ran out; the barriers' votes make it everyone's
+        bool fail = false;  // a wait of this thread ran out: no more waits until the item's vote makes it everyone's
         for (int i = 0;; ++i) {
             const Item it = take_item(i, fail);
             if (!fail && it.blocks == 0)
@@ -750,7 +770,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
                 if (lane == 0)
                     mbar_arrive(smem_u32(&sm->q_ready));
             }
-            fail = named_barrier_any(1, SOFT_THREADS, fail);  // row_scale of this item is written
+            fail = named_barrier_any(5, SOFT_THREADS, fail);  // row_scale of this item is written
             if (fail)
                 break;
             const bool live = row < it.rows, warp_live = quarter * 32 < it.rows;
@@ -771,23 +791,29 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
                 __syncwarp();
                 tc_fence_after();
                 const uint32_t scol = tmem + A::S_COL + buf * KEY_BLOCK + half * 64 + lanes;
-                uint32_t v[64];
                 float mine = -INFINITY, turn = 1.0f;
                 if (warp_live) {
+                    if (__any_sync(0xFFFFFFFFu, vis < 64)) {  // out of sight: -inf in place of the scores
+#pragma unroll 1
+                        for (int c32 = 0; c32 < 64; c32 += 32) {
+                            uint32_t v[32];
+                            tc_ld_32x32b_x32(scol + c32, v);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                v[e] = c32 + e < vis ? v[e] : 0xFF800000u;
+                            tc_st_32x32b_x32(scol + c32, v);
+                        }
+                        tc_wait_st();
+                    }
+                    uint32_t v[64];
                     tc_ld_32x32b_x64(scol, v);
                     tc_wait_ld();
-                    if (__any_sync(0xFFFFFFFFu, vis < 64)) {
-#pragma unroll
-                        for (int e = 0; e < 64; ++e)
-                            v[e] = e < vis ? v[e] : 0xFF800000u;
-                    }
                     mine = block_max64(v);
                     sm->red[buf][half][row] = make_float2(mine, so_far);
                 }
                 vis -= live ? KEY_BLOCK : 0;
-                fail = named_barrier_any(1, SOFT_THREADS, fail);
-                if (fail)
-                    break;
+                named_barrier_sync(1 + quarter, 64);  // the two warps of these rows
                 if (warp_live) {
                     const float2 other = sm->red[buf][half ^ 1][row];
                     const float tm = fmaxf(mine, other.x) * f;
@@ -813,43 +839,46 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
                     if (lane == 0)
                         mbar_arrive(smem_u32(&sm->turn_ready[buf]));
                 }
-                if (warp_live) {
-                    const uint64_t bb = pack2(P_SHIFT - ref, P_SHIFT - ref);
-                    uint64_t sum_b = 0;
-                    uint32_t hi[16], lo[16];
+                const uint64_t bb = pack2(P_SHIFT - ref, P_SHIFT - ref);
+                uint64_t sum_b = 0;
+                // Scores are read from TMEM a second time, 32 at a time, instead of being held: the loop's code is
+                // half as long, and the warps' loops together have to fit the instruction cache.
+#pragma unroll 1
+                for (int c32 = 0; c32 < 2; ++c32) {
+                    if (warp_live) {
+                        uint32_t v[32], hi[8], lo[8];
+                        tc_ld_32x32b_x32(scol + c32 * 32, v);
+                        tc_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        uint64_t x[2], y[2], z[2];
+                        for (int k = 0; k < 8; ++k) {
+                            uint64_t x[2], y[2], z[2];
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float a, b;
-                            unpack2(fma2(pack2u(v[4 * k + 2 * e], v[4 * k + 2 * e + 1]), ff, bb), a, b);
-                            a = exp2_fast(a);
-                            b = exp2_fast(b);
-                            x[e] = pack2(a, b);
-                            y[e] = pack2u(__float_as_uint(a) & 0xFFF00000u, __float_as_uint(b) & 0xFFF00000u);
-                            z[e] = fma2(y[e], neg, x[e]);
+                            for (int e = 0; e < 2; ++e) {
+                                const uint64_t t = fma2(pack2u(v[4 * k + 2 * e], v[4 * k + 2 * e + 1]), ff, bb);
+                                // three of four pairs on the special-function unit, one on the FMA pipe
+                                x[e] = (2 * k + e) % 4 == 3 ? exp2_poly2(t) : exp2_fast2(t);
+                                y[e] = x[e] & 0xFFF00000FFF00000ull;
+                                z[e] = fma2(y[e], neg, x[e]);
+                            }
+                            sum2 = add2(sum2, x[0]);
+                            sum_b = add2(sum_b, x[1]);
+                            hi[k] = e4m3x4_of(y[0], y[1]);
+                            lo[k] = e4m3x4_of(z[0], z[1]);
                         }
-                        sum2 = add2(sum2, x[0]);
-                        sum_b = add2(sum_b, x[1]);
-                        hi[k] = e4m3x4_of(y[0], y[1]);
-                        lo[k] = e4m3x4_of(z[0], z[1]);
+                        tc_st_32x32b_x8(scol + c32 * 8, hi);
+                        tc_st_32x32b_x8(scol + 16 + c32 * 8, lo);
+                        tc_wait_st();
                     }
-                    sum2 = add2(sum2, sum_b);
-                    float sa, sb;
-                    unpack2(sum2, sa, sb);
-                    so_far = sa + sb;
-                    tc_st_32x32b_x16(scol, hi);
-                    tc_st_32x32b_x16(scol + 16, lo);
-                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(smem_u32(c32 ? &sm->p_rest[buf] : &sm->p_ready[buf]));
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_u32(&sm->p_ready[buf]));
+                sum2 = add2(sum2, sum_b);
+                float sa, sb;
+                unpack2(sum2, sa, sb);
+                so_far = sa + sb;
             }
-            if (fail)
-                break;
             sm->sum[i & 1][half][row] = so_far;
             if (half == 0)
                 sm->ref[i & 1][row] = top > -INFINITY ? ref : -INFINITY;

@@ -12,6 +12,18 @@
 namespace nvfp4 {
 namespace attn {
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
 // D[tmem] (+)= A[smem] x B[smem], 8-bit operands, fp32 accumulator.
 __device__ __forceinline__ void tc_mma_f8_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                              uint32_t accumulate)
@@ -151,6 +163,14 @@ __device__ __forceinline__ uint32_t e4m3x4_of(uint64_t ab, uint64_t cd)
     return f32_to_e4m3x4(a, b, c, d);
 }
 
+// 32 lanes x 8 consecutive 32-bit columns from registers.
+__device__ __forceinline__ void tc_st_32x32b_x8(uint32_t taddr, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 // Two E4M3 codes from two f16 values and back (exact).
 __device__ __forceinline__ uint32_t f16x2_to_e4m3x2(__half2 x)
 {
@@ -197,6 +217,40 @@ __device__ __forceinline__ float exp2_fast(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// 2^x of a pair on the special-function unit.
+__device__ __forceinline__ uint64_t exp2_fast2(uint64_t t)
+{
+    float a, b;
+    unpack2(t, a, b);
+    return pack2(exp2_fast(a), exp2_fast(b));
+}
+
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// 2^x of a pair on the FMA and integer pipes, for x < 127: x = n + f with n
+// the nearest integer (adding 1.5 * 2^23 leaves n in the low mantissa bits)
+// and |f| <= 1/2; 2^f by the polynomial of degree 3 that is best in relative
+// error there (below 2^-13.7), and 2^n from its bits.  x is held at -100,
+// where the result stands for zero; a NaN stays one.
+__device__ __forceinline__ uint64_t exp2_poly2(uint64_t t)
+{
+    float a, b, na, nb;
+    unpack2(t, a, b);
+    t = pack2(max_nan(a, -100.0f), max_nan(b, -100.0f));
+    const uint64_t n = add2(t, pack2(12582912.0f, 12582912.0f));
+    const uint64_t f = fma2(add2(n, pack2(-12582912.0f, -12582912.0f)), pack2(-1.0f, -1.0f), t);
+    uint64_t y = fma2(f, pack2(0.0551716462f, 0.0551716462f), pack2(0.24261117f, 0.24261117f));
+    y = fma2(f, y, pack2(0.693260968f, 0.693260968f));
+    y = fma2(f, y, pack2(0.999928057f, 0.999928057f));
+    unpack2(n, na, nb);
+    return mul2(y, pack2u(0x3F800000u + (__float_as_uint(na) << 23), 0x3F800000u + (__float_as_uint(nb) << 23)));
 }
 
 }  // namespace attn
