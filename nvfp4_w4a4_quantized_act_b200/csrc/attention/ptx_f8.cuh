@@ -61,36 +61,29 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
-// mbar_wait_bounded of ptx_sm100.cuh for kernels with many waiting warps: each
-// try suspends the thread for up to `kSuspendNs` instead of polling, so that
-// waiting warps leave the issue slots to the working ones.
-constexpr uint32_t kSuspendNs = 50000;
-
-__device__ __forceinline__ bool mbar_try_wait_suspended(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(kSuspendNs)
-        : "memory");
-    return ok != 0;
-}
-
-__device__ __noinline__ bool mbar_wait_suspended(uint32_t bar, uint32_t parity, uint64_t limit_ns)
+// mbar_wait_bounded of ptx_sm100.cuh with the clock out of the way: reading it
+// before the second try would delay a wait that is over a moment later by
+// hundreds of cycles, and the slow path is one function instead of a copy at
+// every wait (the warps' loops share the instruction cache).
+__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, uint64_t limit_ns)
 {
     const uint64_t t0 = global_timer_ns();
-    while (!mbar_try_wait_suspended(bar, parity))
-        if (global_timer_ns() - t0 > limit_ns)
-            return false;
-    return true;
+    do {
+#pragma unroll 1
+        for (int i = 0; i < 256; ++i)
+            if (mbar_try_wait(bar, parity))
+                return true;
+    } while (global_timer_ns() - t0 <= limit_ns);
+    return false;
 }
 
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns)
 {
-    return mbar_try_wait(bar, parity) || mbar_wait_suspended(bar, parity, limit_ns);
+#pragma unroll 1
+    for (int i = 0; i < 256; ++i)
+        if (mbar_try_wait(bar, parity))
+            return true;
+    return mbar_wait_slow(bar, parity, limit_ns);
 }
 
 // Barrier over `count` threads that returns, to all of them alike, whether

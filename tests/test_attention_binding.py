@@ -148,8 +148,8 @@ class _Recorder:
 def rec(monkeypatch):
     r = _Recorder(ops.lib())
     monkeypatch.setattr(ops, "lib", lambda: r)
-    monkeypatch.setattr(ops, "_require_cuda", lambda *ts: None)
-    monkeypatch.setattr(ops, "_stream", lambda stream=None: None)
+    monkeypatch.setattr(ops, "_device_of", lambda t: -1)  # CPU tensors stand in for device ones
+    monkeypatch.setattr(ops, "_stream_ptr", lambda stream, dev: None)
     return r
 
 
@@ -217,6 +217,55 @@ BAD = {
     "attend: strided workspace": lambda: ops.fp8_kv_attention(Q, *_cache(), ws=torch.zeros(1 << 27, dtype=torch.uint8)[::2]),
     "attend: amax too small": lambda: ops.fp8_kv_attention(Q, *_cache(), out_amax=torch.zeros(2, dtype=torch.uint8)),
 }
+
+
+def test_packed_structs_have_the_layout_of_the_header(rec):
+    """The host structs that a call packs, read back field by field."""
+    seen = {}
+
+    def keep(name, *specs):
+        def call(*a):
+            seen[name] = [kind.from_buffer_copy(ctypes.string_at(a[i], ctypes.sizeof(kind))) for i, kind in specs]
+            return 0
+        return call
+    for name, specs in (("nvfp4_qk_norm_rope", ((0, ops.Heads), (1, ops.Heads), (2, ops.Heads), (3, ops.Heads), (7, ops.NormRope))),
+                        ("nvfp4_fp8_kv_append", ((0, ops.Heads), (1, ops.Heads), (3, ops.KvPages), (4, ops.KvBatch), (6, ops.NormRope))),
+                        ("nvfp4_fp8_kv_attention", ((0, ops.Heads), (1, ops.Heads), (2, ops.Heads), (4, ops.KvPages), (5, ops.KvBatch),
+                                                    (6, ops.AttentionOpts)))):
+        rec.__dict__[name] = keep(name, *specs)
+
+    def same(x, **want):
+        for k, v in want.items():
+            assert getattr(x, k) == (v if v != 0 or isinstance(v, float) or "stride" in k or k == "flags" else None), k
+    ko, qo, g = K.clone(), Q.clone(), Q.clone()
+    ops.qk_norm_rope(Q, K, POS, F, W, None, eps=0.25, plus_one=True, q_out=qo, k_out=ko)
+    q, k, q2, k2, nr = seen["nvfp4_qk_norm_rope"]
+    same(q, data=Q.data_ptr(), token_stride=24 * 256, head_stride=256, heads=24)
+    same(k, data=K.data_ptr(), token_stride=4 * 256, head_stride=256, heads=4)
+    same(q2, data=qo.data_ptr(), heads=24)
+    same(k2, data=ko.data_ptr(), heads=4)
+    same(nr, q_weight=W.data_ptr(), k_weight=0, inv_freq=F.data_ptr(), rotary_dim=64, eps=0.25, flags=8)
+    kp, vp = P, torch.zeros(8, 4, 16, 256, dtype=torch.uint8).transpose(1, 2)
+    two = torch.ones(1)
+    pages = dict(k_pages=kp.data_ptr(), v_pages=vp.data_ptr(), k_scale=ONE.data_ptr(), v_scale=two.data_ptr(), k_page_stride=16384,
+                 k_token_stride=1024, k_head_stride=256, v_page_stride=16384, v_token_stride=256, v_head_stride=4096, num_pages=8,
+                 page_size=16, kv_heads=4, head_dim=256)
+    batch = dict(page_table=TABLE.data_ptr(), cu_tokens=CU.data_ptr(), seq_lens=LENS.data_ptr(), table_stride=4, num_seqs=2, max_pages=4)
+    ops.fp8_kv_append(K, ko, kp, vp, ONE, two, TABLE, CU, LENS, inv_freq=F, k_weight=W)
+    k, v, pg, bt, nr = seen["nvfp4_fp8_kv_append"]
+    same(k, data=K.data_ptr())
+    same(v, data=ko.data_ptr())
+    same(pg, **pages)
+    same(bt, **batch)
+    same(nr, q_weight=0, k_weight=W.data_ptr(), inv_freq=F.data_ptr(), rotary_dim=64, flags=0)
+    ops.fp8_kv_attention(Q, kp, vp, ONE, two, TABLE, CU, LENS, softmax_scale=0.5, gate=g, out=qo)
+    q, gt, o, pg, bt, op = seen["nvfp4_fp8_kv_attention"]
+    same(q, data=Q.data_ptr())
+    same(gt, data=g.data_ptr())
+    same(o, data=qo.data_ptr())
+    same(pg, **pages)
+    same(bt, **batch)
+    same(op, softmax_scale=0.5, flags=0)
 
 
 @pytest.mark.parametrize("case", sorted(GOOD))
