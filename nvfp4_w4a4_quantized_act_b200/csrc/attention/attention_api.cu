@@ -204,12 +204,15 @@ int64_t part_rows(int64_t tokens, int64_t group) { return std::min<int64_t>(attn
 
 int64_t part_ml_bytes(int64_t rows) { return (attn::CTAS * 2 * rows * 8 + 255) / 256 * 256; }
 
-// Tokens of a block of the row kernels: several once every SM has blocks
-// enough, so that the block's angles cost one wave of its threads.
-int block_tokens(int64_t tokens, int sm_count)
+// Heads that one warp of the row kernels takes: one while the rows do not
+// fill the GPU, then as many as make a few warps for every place, up to
+// `most`, sharing the token's angles.
+int unit_heads(int64_t rows, int64_t heads, int sm_count, int64_t most)
 {
-    return tokens >= int64_t(sm_count) * 8 * attn::BLOCK_TOKENS ? attn::BLOCK_TOKENS : 1;
+    return static_cast<int>(std::max<int64_t>(1, std::min({most, heads, rows / (int64_t(sm_count) * 64)})));
 }
+
+int64_t row_blocks(int64_t units) { return cdiv(units, attn::ROW_WARPS); }
 
 }  // namespace
 
@@ -260,10 +263,13 @@ extern "C" int nvfp4_qk_norm_rope(const nvfp4_heads *q, const nvfp4_heads *k, co
     p.eps = norm_rope->eps;
     p.one = (norm_rope->flags & NVFP4_NORM_PLUS_ONE) ? 1.0f : 0.0f;
     p.tokens = static_cast<int32_t>(tokens);
-    p.block_tokens = block_tokens(tokens, d.sm_count);
-    const dim3 grid(static_cast<unsigned>(cdiv(tokens, p.block_tokens)));
+    const int64_t rows = tokens * (p.in[0].heads + p.in[1].heads) * head_dim / 256;
+    p.unit_heads = unit_heads(rows, std::max(p.in[0].heads, p.in[1].heads), d.sm_count, 8) * static_cast<int>(256 / head_dim);
+    p.units[0] = static_cast<int32_t>(cdiv(p.in[0].heads, p.unit_heads));
+    p.units[1] = static_cast<int32_t>(cdiv(p.in[1].heads, p.unit_heads));
+    const dim3 grid(static_cast<unsigned>(row_blocks(tokens * (p.units[0] + p.units[1]))));
     launch(head_dim == 256 ? attn::qk_norm_rope_kernel<256> : attn::qk_norm_rope_kernel<128>, grid,
-           dim3(attn::ROW_THREADS), 0, static_cast<cudaStream_t>(stream), p);
+           dim3(attn::ROW_WARPS * 32), 0, static_cast<cudaStream_t>(stream), p);
     nvfp4::host::count_launch();
     return launch_ok();
 }
@@ -314,12 +320,14 @@ extern "C" int nvfp4_fp8_kv_append(const nvfp4_heads *k, const nvfp4_heads *v, i
     p.half = norm_rope->rotary_dim / 2;
     p.eps = norm_rope->eps;
     p.one = (norm_rope->flags & NVFP4_NORM_PLUS_ONE) ? 1.0f : 0.0f;
-    p.block_tokens = block_tokens(tokens, d.sm_count);
     p.batch = batch_view(batch, cache, tokens);
     p.status = d.status;
-    const dim3 grid(static_cast<unsigned>(cdiv(tokens, p.block_tokens)));
+    const int64_t rows = tokens * cache->kv_heads * 2 * cache->head_dim / 256;
+    p.unit_heads = unit_heads(rows, cache->kv_heads, d.sm_count, 4) * (256 / cache->head_dim);
+    p.units = static_cast<int32_t>(cdiv(cache->kv_heads, p.unit_heads));
+    const dim3 grid(static_cast<unsigned>(row_blocks(tokens * p.units)));
     launch(cache->head_dim == 256 ? attn::kv_append_kernel<256> : attn::kv_append_kernel<128>, grid,
-           dim3(attn::ROW_THREADS), 0, static_cast<cudaStream_t>(stream), p);
+           dim3(attn::ROW_WARPS * 32), 0, static_cast<cudaStream_t>(stream), p);
     nvfp4::host::count_launch();
     return launch_ok();
 }

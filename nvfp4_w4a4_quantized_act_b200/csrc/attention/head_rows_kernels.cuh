@@ -7,13 +7,14 @@
 //   out = bf16_RNE(y)   or   code = E4M3_RNE_satfinite(fl32(y / scale))
 //
 // Both are bound by memory: a row is read once and written once, held in
-// registers in between.  A row of 128 (256) elements is taken by 16 (32)
-// lanes, 8 elements = one 16-byte load each, so a warp's load covers 512
-// contiguous bytes; the mean is a 4- (5-) step shuffle, and since R/2 is a
-// multiple of 8 an element's partner sits at the same place of another lane.
-// The angle is the expensive part -- an fp64 product and reduction and a
-// sincosf -- and the same for every head, so a block computes the angles of
-// its tokens once, one thread each, into shared memory.
+// registers in between.  A warp takes one token and a few of its heads, and
+// needs no other warp: a row of 256 (128) elements is held by 32 (16) lanes, 8
+// elements each.  The lanes of the rotated part hold 4 elements of the first
+// half and their 4 partners of the second, so a pair turns inside a lane; the
+// others hold 8 neighbours.  The angle is the expensive part (an fp64 product
+// and reduction, a sine and cosine) and the same for every head: the warp
+// computes its token's angles once, a lane each, while the first rows are on
+// their way.
 #pragma once
 
 #include <cstdint>
@@ -26,20 +27,20 @@
 namespace nvfp4 {
 namespace attn {
 
-constexpr int ROW_THREADS = 256;
+constexpr int ROW_WARPS = 4;        // warps of a block
 constexpr int MAX_HALF = 128;       // rotated pairs of a head (head_dim <= 256)
-constexpr int BLOCK_TOKENS = 4;     // tokens of a block for large batches
 
-// cos and sin of pos * f.  fp64 holds the product of a 31-bit position and a
-// 24-bit frequency to 2^-53 of its value; after whole turns are taken off the
-// remainder is below pi and fp32 keeps it to 2^-25 of pi.
+// cos and sin of pos * f.  The product of a 31-bit position and a 24-bit
+// frequency is held in fp64, multiplied by 1 / 2 pi (in two parts) and reduced
+// to less than half a turn by exact steps; fp32 keeps the rest to 2^-25.
 __device__ __forceinline__ float2 rotation(int32_t pos, float f)
 {
     const double a = static_cast<double>(pos) * static_cast<double>(f);
-    const double turns = rint(a * 0.15915494309189533577);
-    const float r = static_cast<float>(fma(turns, -2.4492935982947064e-16, fma(turns, -6.283185307179586232, a)));
+    const double hi = 0.15915494309189535, lo = -9.839338337591243e-18;  // hi + lo = 1 / 2 pi
+    const double turns = rint(a * hi);
+    const float t = static_cast<float>(fma(a, lo, fma(a, hi, -turns)));
     float2 cs;
-    sincosf(r, &cs.y, &cs.x);
+    sincospif(2.0f * t, &cs.y, &cs.x);
     return cs;
 }
 
@@ -64,52 +65,81 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8])
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Norm and rotation of one row spread over D / 8 lanes, in place.  `w`: the
-// lane's 8 norm weights; cs: the token's rotations; col: the lane's first
-// element.  All 32 lanes call it.
+// Where a lane's 8 elements of a row lie: 4 at `a` and 4 at `b`; rotated: b is
+// a's partner.
+struct LaneMap {
+    int a, b;
+    bool turned;
+
+    __device__ __forceinline__ LaneMap(int lane_of_row, int half)
+    {
+        turned = lane_of_row < (half >> 2);
+        a = lane_of_row * (turned ? 4 : 8);
+        b = turned ? half + a : a + 4;
+    }
+};
+
+__device__ __forceinline__ uint4 load_row(const uint16_t *row, const LaneMap &m)
+{
+    const uint2 u = *reinterpret_cast<const uint2 *>(row + m.a), v = *reinterpret_cast<const uint2 *>(row + m.b);
+    return make_uint4(u.x, u.y, v.x, v.y);
+}
+
+// The token's rotations to shared memory (one warp's share), then the lane's 4.
+__device__ __forceinline__ void load_rotations(float2 *cs, int32_t pos, const float *inv_freq, int half, const LaneMap &m,
+                                               int lane, float (&c)[4], float (&s)[4])
+{
+    for (int i = lane; i < half; i += 32)
+        cs[i] = rotation(pos, __ldg(inv_freq + i));
+    __syncwarp();
+    if (m.turned) {
+        const float4 u = *reinterpret_cast<const float4 *>(cs + m.a), v = *reinterpret_cast<const float4 *>(cs + m.a + 2);
+        c[0] = u.x, s[0] = u.y, c[1] = u.z, s[1] = u.w, c[2] = v.x, s[2] = v.y, c[3] = v.z, s[3] = v.w;
+    }
+}
+
+// Norm and rotation of one row spread over D / 8 lanes, in place.  All 32
+// lanes call it (with D = 128 for two rows).
 template <int D>
-__device__ __forceinline__ void norm_rotate(float (&x)[8], bool norm, const float (&w)[8], float eps, const float2 *cs,
-                                            int half, int col, int lane)
+__device__ __forceinline__ void norm_rotate(float (&x)[8], bool norm, const float (&w)[8], float eps, bool turned,
+                                            const float (&c)[4], const float (&s)[4])
 {
     if (norm) {
-        float ss = 0.0f;
+        float ss = 0.0f, st = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 4; ++i) {
             ss = fmaf(x[i], x[i], ss);
+            st = fmaf(x[i + 4], x[i + 4], st);
+        }
+        ss += st;
 #pragma unroll
         for (int o = D / 16; o > 0; o >>= 1)
             ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-        const float r = 1.0f / sqrtf(ss * (1.0f / D) + eps);
+        const float r = rsqrtf(ss * (1.0f / D) + eps);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             x[i] = x[i] * r * w[i];
     }
-    if (half > 0) {
-        const bool low = col < half, turned = col < 2 * half;
-        const int src = turned ? (low ? lane + (half >> 3) : lane - (half >> 3)) : lane;
-        const float2 *my = cs + (turned ? (low ? col : col - half) : 0);
+    if (turned) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float other = __shfl_sync(0xFFFFFFFFu, x[i], src);
-            if (turned) {
-                const float2 c = my[i];
-                x[i] = low ? fmaf(x[i], c.x, -(other * c.y)) : fmaf(x[i], c.x, other * c.y);
-            }
+        for (int i = 0; i < 4; ++i) {
+            const float a = x[i], b = x[i + 4];
+            x[i] = fmaf(a, c[i], -(b * s[i]));
+            x[i + 4] = fmaf(b, c[i], a * s[i]);
         }
     }
 }
 
-__device__ __forceinline__ void load_weights(const uint16_t *w, int col, float one, float (&out)[8])
+__device__ __forceinline__ void load_weights(const uint16_t *w, const LaneMap &m, float one, float (&out)[8])
 {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         out[i] = 1.0f;
     if (w != nullptr) {
-        float x[8];
-        unpack8(__ldg(reinterpret_cast<const uint4 *>(w + col)), x);
+        unpack8(load_row(w, m), out);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            out[i] = x[i] + one;
+            out[i] += one;
     }
 }
 
@@ -128,53 +158,54 @@ struct NormRopeParams {
     float eps;
     float one;                // 1 with NVFP4_NORM_PLUS_ONE, else 0
     int32_t tokens;
-    int32_t block_tokens;
+    int32_t unit_heads;       // heads of a warp
+    int32_t units[2];         // warps of a token: for its queries, for its keys
 };
 
 template <int D>
-__global__ void __launch_bounds__(ROW_THREADS) qk_norm_rope_kernel(const NormRopeParams p)
+__global__ void __launch_bounds__(ROW_WARPS * 32) qk_norm_rope_kernel(const NormRopeParams p)
 {
     constexpr int LANES = D / 8;               // lanes of a row
     constexpr int GROUP = 32 / LANES;          // rows of a warp at a time
-    constexpr int STEP = ROW_THREADS / LANES;  // rows of the block at a time
-    __shared__ float2 cs[BLOCK_TOKENS * MAX_HALF];
+    __shared__ alignas(16) float2 cs[ROW_WARPS][MAX_HALF];
     grid_dep_wait();
     grid_dep_launch_dependents();
-    const int lane = threadIdx.x & 31;
-    const int col = (lane % LANES) * 8;
-    const int heads = p.in[0].heads + p.in[1].heads;
-    const int t0 = blockIdx.x * p.block_tokens;
-    const int nt = min(p.block_tokens, p.tokens - t0);
-    for (int i = threadIdx.x; i < nt * p.half; i += ROW_THREADS) {
-        const int t = i / p.half;
-        cs[t * MAX_HALF + (i - t * p.half)] = rotation(__ldg(p.positions + t0 + t), __ldg(p.inv_freq + (i - t * p.half)));
-    }
-    float w[2][8];
-    load_weights(p.weight[0], col, p.one, w[0]);
-    load_weights(p.weight[1], col, p.one, w[1]);
-    __syncthreads();
-    const int rows = nt * heads;
-    for (int base = (threadIdx.x >> 5) * GROUP; base < rows; base += STEP) {
-        const int row = base + lane / LANES;
-        const bool live = row < rows;
-        const int t = live ? row / heads : 0;
-        int h = live ? row - t * heads : 0;
-        const int which = h >= p.in[0].heads;
-        h -= which ? p.in[0].heads : 0;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per = p.units[0] + p.units[1];
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * ROW_WARPS + warp;
+    const int t = static_cast<int>(unit / per);
+    if (t >= p.tokens)
+        return;
+    int u = static_cast<int>(unit - static_cast<int64_t>(t) * per);
+    const int which = u >= p.units[0];
+    u -= which ? p.units[0] : 0;
+    const HeadRows in = p.in[which], out = p.out[which];
+    const int h1 = min((u + 1) * p.unit_heads, in.heads);
+    const LaneMap m(lane % LANES, p.half);
+    const uint16_t *src = in.data + t * in.token_stride;
+    uint16_t *dst = const_cast<uint16_t *>(out.data) + t * out.token_stride;
+    int h = u * p.unit_heads + lane / LANES;
+    uint4 v = make_uint4(0, 0, 0, 0), next = v;
+    if (h < h1)
+        v = load_row(src + h * in.head_stride, m);
+    if (h + GROUP < h1)
+        next = load_row(src + (h + GROUP) * in.head_stride, m);
+    float w[8], c[4], s[4];
+    load_weights(p.weight[which], m, p.one, w);
+    if (p.half > 0)
+        load_rotations(cs[warp], __ldg(p.positions + t), p.inv_freq, p.half, m, lane, c, s);
+    for (int i = u * p.unit_heads; i < h1; i += GROUP, h += GROUP) {  // alike for all lanes
         float x[8];
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (live)
-            v = *reinterpret_cast<const uint4 *>(p.in[which].data + (t0 + t) * p.in[which].token_stride +
-                                                  h * p.in[which].head_stride + col);
         unpack8(v, x);
-        float wr[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            wr[i] = which ? w[1][i] : w[0][i];
-        norm_rotate<D>(x, p.weight[which] != nullptr, wr, p.eps, cs + t * MAX_HALF, p.half, col, lane);
-        if (live)
-            *reinterpret_cast<uint4 *>(const_cast<uint16_t *>(p.out[which].data) + (t0 + t) * p.out[which].token_stride +
-                                       h * p.out[which].head_stride + col) = pack8(x);
+        v = next;
+        if (h + 2 * GROUP < h1)
+            next = load_row(src + (h + 2 * GROUP) * in.head_stride, m);
+        norm_rotate<D>(x, p.weight[which] != nullptr, w, p.eps, m.turned, c, s);
+        if (h < h1) {
+            const uint4 y = pack8(x);
+            *reinterpret_cast<uint2 *>(dst + h * out.head_stride + m.a) = make_uint2(y.x, y.y);
+            *reinterpret_cast<uint2 *>(dst + h * out.head_stride + m.b) = make_uint2(y.z, y.w);
+        }
     }
 }
 
@@ -189,7 +220,7 @@ struct AppendParams {
     int32_t half;
     float eps;
     float one;
-    int32_t block_tokens;
+    int32_t unit_heads, units;
     BatchView batch;
     uint32_t *status;
 };
@@ -205,86 +236,95 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
 
 __device__ __forceinline__ bool valid_scale(float s) { return s > 0.0f && s <= 3.40282347e38f; }
 
+// Codes of 8 elements divided by s (inv = RN(1 / s)), the IEEE quotients.
+__device__ __forceinline__ uint2 codes8(float (&x)[8], float s, float inv)
+{
+    float big = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        big = fmaxf(big, fabsf(x[i]));
+    if (div_shared_ok(s, big)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            x[i] = div_shared(x[i], s, inv);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            x[i] = __fdiv_rn(x[i], s);
+    }
+    return make_uint2(e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7]));
+}
+
 template <int D>
-__global__ void __launch_bounds__(ROW_THREADS) kv_append_kernel(const AppendParams p)
+__global__ void __launch_bounds__(ROW_WARPS * 32) kv_append_kernel(const AppendParams p)
 {
     constexpr int LANES = D / 8;
     constexpr int GROUP = 32 / LANES;
-    constexpr int STEP = ROW_THREADS / LANES;
-    __shared__ float2 cs[BLOCK_TOKENS * MAX_HALF];
-    __shared__ int64_t slot[BLOCK_TOKENS];  // page << 32 | row in the page; -1: the token is not cached
-    __shared__ int32_t turn[BLOCK_TOKENS];  // position of the rotation
+    __shared__ alignas(16) float2 cs[ROW_WARPS][MAX_HALF];
     grid_dep_wait();
     grid_dep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int col = (lane % LANES) * 8;
     const float s0 = __ldg(p.scale[0]), s1 = __ldg(p.scale[1]);
     if (!valid_scale(s0) || !valid_scale(s1)) {
         if (blockIdx.x == 0 && threadIdx.x == 0)
             atomicOr(p.status, kStatusNonFinite);
         return;
     }
-    const int t0 = blockIdx.x * p.block_tokens;
-    const int nt = min(p.block_tokens, p.batch.tokens - t0);
-    if (warp < nt) {  // one warp finds one token's place
-        const int t = t0 + warp;
-        const int b = warp_find_seq(p.batch, t, lane);
-        if (lane == 0) {
-            bool bad = false;
-            const Seq s = load_seq(p.batch, b, bad);
-            const int j = t - s.first;
-            const int pos = s.len - s.fresh + j;
-            int64_t at = -1;
-            if (j >= 0 && j < s.fresh && pos >= 0) {
-                const int32_t id = __ldg(p.batch.table + b * p.batch.table_stride + (pos >> p.batch.page_shift));
-                if (id >= 0 && id < p.batch.num_pages)
-                    at = (static_cast<int64_t>(id) << 32) | (pos & ((1 << p.batch.page_shift) - 1));
-                else
-                    bad = true;
-            }
-            slot[warp] = at;
-            turn[warp] = p.positions != nullptr ? __ldg(p.positions + t) : max(pos, 0);
-            if (bad)
-                atomicOr(p.status, kStatusBadIndex);
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * ROW_WARPS + warp;
+    const int t = static_cast<int>(unit / p.units);
+    if (t >= p.batch.tokens)
+        return;
+    const int u = static_cast<int>(unit - static_cast<int64_t>(t) * p.units);
+    const int h1 = min((u + 1) * p.unit_heads, p.in[0].heads);
+    const LaneMap m(lane % LANES, p.half);
+    const LaneMap plain(lane % LANES, 0);
+    const uint16_t *k_src = p.in[0].data + t * p.in[0].token_stride, *v_src = p.in[1].data + t * p.in[1].token_stride;
+    int h = u * p.unit_heads + lane / LANES;
+    // the first rows are on their way while the token's place is looked up
+    uint4 kv = make_uint4(0, 0, 0, 0), vv = kv;
+    if (h < h1) {
+        kv = load_row(k_src + h * p.in[0].head_stride, m);
+        vv = load_row(v_src + h * p.in[1].head_stride, plain);
+    }
+    const int b = warp_find_seq(p.batch, t, lane);
+    bool bad = false;
+    const Seq seq = load_seq(p.batch, b, bad);
+    const int j = t - seq.first, pos = seq.len - seq.fresh + j;
+    int64_t id = -1;
+    if (j >= 0 && j < seq.fresh && pos >= 0) {
+        id = __ldg(p.batch.table + b * p.batch.table_stride + (pos >> p.batch.page_shift));
+        if (id < 0 || id >= p.batch.num_pages) {
+            bad = true;
+            id = -1;
         }
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < nt * p.half; i += ROW_THREADS) {
-        const int t = i / p.half;
-        cs[t * MAX_HALF + (i - t * p.half)] = rotation(turn[t], __ldg(p.inv_freq + (i - t * p.half)));
-    }
-    float w[8];
-    load_weights(p.weight, col, p.one, w);
-    __syncthreads();
-    const int heads = p.in[0].heads;
-    const int rows = nt * heads * 2;
-    for (int base = warp * GROUP; base < rows; base += STEP) {
-        const int row = base + lane / LANES;
-        const bool live = row < rows;
-        const int t = live ? row / (2 * heads) : 0;
-        int h = live ? row - t * 2 * heads : 0;
-        const int which = h >= heads;
-        h -= which ? heads : 0;
-        const int64_t at = slot[t];
-        float x[8];
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (live && at >= 0)
-            v = __ldg(reinterpret_cast<const uint4 *>(p.in[which].data + (t0 + t) * p.in[which].token_stride +
-                                                      h * p.in[which].head_stride + col));
-        unpack8(v, x);
-        float y[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            y[i] = x[i];
-        norm_rotate<D>(y, p.weight != nullptr, w, p.eps, cs + t * MAX_HALF, p.half, col, lane);
-        const float s = which ? s1 : s0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            y[i] = __fdiv_rn(which ? x[i] : y[i], s);
-        if (live && at >= 0)
-            *reinterpret_cast<uint2 *>(p.pages[which] + (at >> 32) * p.page_stride[which] +
-                                       (at & 0xFFFFFFFF) * p.token_stride[which] + h * p.head_stride[which] + col) =
-                make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
+    if (bad && lane == 0)
+        atomicOr(p.status, kStatusBadIndex);
+    if (id < 0)
+        return;  // the token belongs to no sequence, or has no place in the cache
+    const int64_t row = pos & ((1 << p.batch.page_shift) - 1);
+    uint8_t *k_dst = p.pages[0] + id * p.page_stride[0] + row * p.token_stride[0];
+    uint8_t *v_dst = p.pages[1] + id * p.page_stride[1] + row * p.token_stride[1];
+    float w[8], c[4], s[4];
+    load_weights(p.weight, m, p.one, w);
+    if (p.half > 0)
+        load_rotations(cs[warp], p.positions != nullptr ? __ldg(p.positions + t) : pos, p.inv_freq, p.half, m, lane, c, s);
+    const float r0 = __frcp_rn(s0), r1 = __frcp_rn(s1);
+    for (int i = u * p.unit_heads; i < h1; i += GROUP, h += GROUP) {  // alike for all lanes
+        float x[8], y[8];
+        unpack8(kv, x);
+        unpack8(vv, y);
+        if (h + GROUP < h1) {
+            kv = load_row(k_src + (h + GROUP) * p.in[0].head_stride, m);
+            vv = load_row(v_src + (h + GROUP) * p.in[1].head_stride, plain);
+        }
+        norm_rotate<D>(x, p.weight != nullptr, w, p.eps, m.turned, c, s);
+        const uint2 kc = codes8(x, s0, r0), vc = codes8(y, s1, r1);
+        if (h < h1) {
+            *reinterpret_cast<uint32_t *>(k_dst + h * p.head_stride[0] + m.a) = kc.x;
+            *reinterpret_cast<uint32_t *>(k_dst + h * p.head_stride[0] + m.b) = kc.y;
+            *reinterpret_cast<uint2 *>(v_dst + h * p.head_stride[1] + plain.a) = vc;
+        }
     }
 }
 

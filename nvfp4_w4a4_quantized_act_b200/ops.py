@@ -593,8 +593,8 @@ def _heads(t, name, dev, like=None, written=False):
         _elsewhere(t, dev, name)
     T, H, D = shape
     s0, s1 = st[0] if T > 1 else 0, st[1] if H > 1 else 0
-    if written and not ((H == 1 or s1 >= D) and (T == 1 or s0 >= (H - 1) * s1 + D)) and \
-            not ((T == 1 or s0 >= D) and (H == 1 or s1 >= (T - 1) * s0 + D)):
+    if written and not ((H <= 1 or s1 >= D) and (T <= 1 or s0 >= (H - 1) * s1 + D)) and \
+            not ((T <= 1 or s0 >= D) and (H <= 1 or s1 >= (T - 1) * s0 + D)):
         raise ValueError(f"{name}'s rows overlap (shape {tuple(shape)}, strides {st})")
     return t.data_ptr(), s0, s1, H
 

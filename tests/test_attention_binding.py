@@ -168,6 +168,8 @@ def _cache(k=P, v=P, ks=ONE, vs=ONE, table=TABLE, cu=CU, lens=LENS):
 
 GOOD = {
     "norm": lambda: ops.qk_norm_rope(Q, K, POS, F, W, W),
+    "norm, no tokens": lambda: ops.qk_norm_rope(Q[:0], K[:0], POS, F, W, W),
+    "attend, no tokens": lambda: ops.fp8_kv_attention(Q[:0], *_cache()),
     "norm, one side, no rotation": lambda: ops.qk_norm_rope(Q, None, None, None, W),
     "norm, heads first": lambda: ops.qk_norm_rope(Q, K, POS, F, q_out=torch.zeros(24, 3, 256, dtype=bf16).transpose(0, 1)),
     "append": lambda: ops.fp8_kv_append(K, K, *_cache(), inv_freq=F, k_weight=W, positions=POS),
