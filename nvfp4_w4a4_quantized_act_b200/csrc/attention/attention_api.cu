@@ -14,6 +14,7 @@
 #include "host.h"
 #include "paged_attention_kernel.cuh"
 #include "paged_batch.cuh"
+#include "paged_decode_kernel.cuh"
 
 namespace {
 
@@ -143,15 +144,19 @@ attn::BatchView batch_view(const nvfp4_kv_batch *b, const nvfp4_kv_pages *c, int
     v.page_shift = log2_of(c->page_size);
     v.tokens = static_cast<int32_t>(tokens);
     v.num_pages = c->num_pages;
+    v.fresh_min = 1;
+    v.fresh_max = INT32_MAX;
+    v.item_cost = 0;
     return v;
 }
 
 // The pages of K or V as a 4-D byte tensor, dimensions in the order of their
 // strides behind the contiguous head_dim; row_at and head_at say where the
-// page's rows and the heads ended up.  A box is one page's rows (128 at most)
+// page's rows and the heads ended up.  A box is one page's rows (box_rows at most)
 // by 128 bytes of one head.
 int make_page_map(const nvfp4::host::Device &d, CUtensorMap *map, const void *base, const nvfp4_kv_pages *c,
-                  int64_t page_stride, int64_t row_stride, int64_t head_stride, int32_t *row_at, int32_t *head_at)
+                  int64_t page_stride, int64_t row_stride, int64_t head_stride, int32_t box_rows, int32_t *row_at,
+                  int32_t *head_at)
 {
     struct Dim {
         int64_t stride, size;
@@ -167,7 +172,7 @@ int make_page_map(const nvfp4::host::Device &d, CUtensorMap *map, const void *ba
         size[i + 1] = static_cast<cuuint64_t>(dims[i].size);
         stride[i] = static_cast<cuuint64_t>(dims[i].stride);
         if (dims[i].which == 0) {
-            box[i + 1] = static_cast<cuuint32_t>(std::min(c->page_size, attn::KEY_BLOCK));
+            box[i + 1] = static_cast<cuuint32_t>(std::min(c->page_size, box_rows));
             *row_at = i + 1;
         } else if (dims[i].which == 1) {
             *head_at = i + 1;
@@ -190,19 +195,43 @@ int allow_smem(int device)
     if (cudaFuncSetAttribute(attn::paged_attention_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              attn::attn_smem_bytes<128>()) != cudaSuccess ||
         cudaFuncSetAttribute(attn::paged_attention_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             attn::attn_smem_bytes<256>()) != cudaSuccess)
+                             attn::attn_smem_bytes<256>()) != cudaSuccess ||
+        cudaFuncSetAttribute(attn::paged_decode_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             attn::decode_smem_bytes<128>()) != cudaSuccess ||
+        cudaFuncSetAttribute(attn::paged_decode_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             attn::decode_smem_bytes<256>()) != cudaSuccess)
         return NVFP4_ERR_CUDA;
     done[device].store(true, std::memory_order_release);
     return NVFP4_OK;
 }
 
-// Workspace: a PartInfo per CTA, then the two parts of each CTA: per row its
+// Workspace: two sets of parts (the tile kernel's, the single-token kernel's).
+// A set: a PartInfo per CTA, then the two parts of each CTA: per row its
 // reference and sum, then its sums of values.
 constexpr int64_t kPartsBytes = (attn::CTAS * sizeof(attn::PartInfo) + 255) / 256 * 256;
 
 int64_t part_rows(int64_t tokens, int64_t group) { return std::min<int64_t>(attn::ROW_TILE / group, tokens) * group; }
 
 int64_t part_ml_bytes(int64_t rows) { return (attn::CTAS * 2 * rows * 8 + 255) / 256 * 256; }
+
+int64_t parts_bytes(int64_t rows, int64_t head_dim)
+{
+    return kPartsBytes + part_ml_bytes(rows) + attn::CTAS * 2 * rows * head_dim * 4;
+}
+
+attn::Parts parts_at(uint8_t *base, int64_t rows)
+{
+    attn::Parts p;
+    p.info = reinterpret_cast<attn::PartInfo *>(base);
+    p.ml = reinterpret_cast<float *>(base + kPartsBytes);
+    p.o = reinterpret_cast<float *>(base + kPartsBytes + part_ml_bytes(rows));
+    p.rows = static_cast<int32_t>(rows);
+    return p;
+}
+
+// Which kernels a call launches, and the cost of their items in keys.
+constexpr int32_t kMixedSeqs = 8, kPadRows = 8;
+constexpr int32_t kTileItemCost = 512, kDecodeItemCost = 128;
 
 // Heads that one warp of the row kernels takes: one while the rows do not
 // fill the GPU, then as many as make a few warps for every place, up to
@@ -338,8 +367,9 @@ extern "C" size_t nvfp4_fp8_kv_attention_workspace_bytes(int64_t tokens, int64_t
     if (check_tokens(tokens) != NVFP4_OK || check_head_dim(head_dim) != NVFP4_OK || q_heads < 1 || kv_heads < 1 ||
         q_heads > kMaxHeads || q_heads % kv_heads != 0 || q_heads / kv_heads > 128)
         return 0;
-    const int64_t rows = part_rows(tokens, q_heads / kv_heads);
-    return static_cast<size_t>(kPartsBytes + part_ml_bytes(rows) + attn::CTAS * 2 * rows * head_dim * 4);
+    const int64_t group = q_heads / kv_heads;
+    return static_cast<size_t>(parts_bytes(part_rows(tokens, group), head_dim) +
+                               (group <= attn::DECODE_ROWS ? parts_bytes(group, head_dim) : 0));
 }
 
 extern "C" int nvfp4_fp8_kv_attention(const nvfp4_heads *q, const nvfp4_heads *gate, const nvfp4_heads *out,
@@ -382,43 +412,66 @@ extern "C" int nvfp4_fp8_kv_attention(const nvfp4_heads *q, const nvfp4_heads *g
     }
     if (tokens == 0 || batch->num_seqs == 0)
         return NVFP4_OK;
-    CUtensorMap tm_k, tm_v;
+    // Sequences with one new token go to the kernel for single tokens where the
+    // heads that share a key fit its rows.  The lengths are on the device, so
+    // the sizes have to say which kernels may find work: as many token rows as
+    // sequences or fewer, all go there (it is right for longer ones too, but
+    // reads their keys again for every token); a batch of some sequences, or
+    // one padded by a few rows, may hold both kinds; else it is prompts alone.
+    const int64_t group = q->heads / cache->kv_heads;
+    const bool single = group <= attn::DECODE_ROWS &&
+                        (batch->num_seqs >= kMixedSeqs || tokens <= int64_t(batch->num_seqs) + kPadRows);
+    const bool tiled = !single || tokens > batch->num_seqs;
     attn::AttnParams p;
-    if (make_page_map(d, &tm_k, cache->k_pages, cache, cache->k_page_stride, cache->k_token_stride,
-                      cache->k_head_stride, &p.k_row_at, &p.k_head_at) != NVFP4_OK ||
-        make_page_map(d, &tm_v, cache->v_pages, cache, cache->v_page_stride, cache->v_token_stride,
-                      cache->v_head_stride, &p.v_row_at, &p.v_head_at) != NVFP4_OK ||
-        allow_smem(d.index) != NVFP4_OK)
-        return NVFP4_ERR_CUDA;
     p.q = rows_of(q);
     p.gate = rows_of(gate);
     p.out = rows_of(out);
     p.k_scale = cache->k_scale;
     p.v_scale = cache->v_scale;
     p.kv_heads = cache->kv_heads;
-    p.group = static_cast<int32_t>(q->heads / cache->kv_heads);
-    p.tile_tokens = attn::ROW_TILE / p.group;
-    p.group_inv = static_cast<uint32_t>((65536 + p.group - 1) / p.group);
+    p.group = static_cast<int32_t>(group);
+    p.group_inv = static_cast<uint32_t>((65536 + group - 1) / group);
     p.softmax_scale = opts->softmax_scale;
     p.batch = batch_view(batch, cache, tokens);
-    p.part_rows = static_cast<int32_t>(part_rows(tokens, p.group));
-    uint8_t *base = static_cast<uint8_t *>(ws);
-    p.parts = reinterpret_cast<attn::PartInfo *>(base);
-    p.part_ml = reinterpret_cast<float *>(base + kPartsBytes);
-    p.part_o = reinterpret_cast<float *>(base + kPartsBytes + part_ml_bytes(p.part_rows));
     p.out_amax = out_amax;
     p.status = d.status;
-    const dim3 join_grid(attn::CTAS, static_cast<unsigned>(cdiv(p.part_rows, attn::JOIN_ROWS)));
-    if (cache->head_dim == 256) {
-        launch(attn::paged_attention_kernel<256>, dim3(attn::CTAS), dim3(attn::ATTN_THREADS),
-               attn::attn_smem_bytes<256>(), s, tm_k, tm_v, p);
-        launch(attn::paged_attention_join_kernel<256>, join_grid, dim3(attn::JOIN_ROWS * 32), 0, s, p);
-    } else {
-        launch(attn::paged_attention_kernel<128>, dim3(attn::CTAS), dim3(attn::ATTN_THREADS),
-               attn::attn_smem_bytes<128>(), s, tm_k, tm_v, p);
-        launch(attn::paged_attention_join_kernel<128>, join_grid, dim3(attn::JOIN_ROWS * 32), 0, s, p);
+    uint8_t *base = static_cast<uint8_t *>(ws);
+    const attn::Parts parts[2] = {
+        parts_at(base, part_rows(tokens, group)),
+        parts_at(base + parts_bytes(part_rows(tokens, group), cache->head_dim), group)};
+    if (allow_smem(d.index) != NVFP4_OK)
+        return NVFP4_ERR_CUDA;
+    int sets = 0;
+    for (int k = 0; k < 2; ++k) {
+        if (!(k == 0 ? tiled : single))
+            continue;
+        CUtensorMap tm_k, tm_v;
+        const int32_t box_rows = k == 0 ? attn::KEY_BLOCK : attn::WARP_KEYS;
+        if (make_page_map(d, &tm_k, cache->k_pages, cache, cache->k_page_stride, cache->k_token_stride,
+                          cache->k_head_stride, box_rows, &p.k_row_at, &p.k_head_at) != NVFP4_OK ||
+            make_page_map(d, &tm_v, cache->v_pages, cache, cache->v_page_stride, cache->v_token_stride,
+                          cache->v_head_stride, box_rows, &p.v_row_at, &p.v_head_at) != NVFP4_OK)
+            return NVFP4_ERR_CUDA;
+        p.parts = parts[k];
+        p.tile_tokens = k == 0 ? attn::ROW_TILE / p.group : 1;
+        p.batch.fresh_min = k == 0 && single ? 2 : 1;
+        p.batch.fresh_max = k == 0 || !tiled ? INT32_MAX : 1;
+        p.batch.item_cost = k == 0 ? kTileItemCost : kDecodeItemCost;
+        if (k == 0)
+            launch(cache->head_dim == 256 ? attn::paged_attention_kernel<256> : attn::paged_attention_kernel<128>,
+                   dim3(attn::CTAS), dim3(attn::ATTN_THREADS),
+                   cache->head_dim == 256 ? attn::attn_smem_bytes<256>() : attn::attn_smem_bytes<128>(), s, tm_k, tm_v, p);
+        else
+            launch(cache->head_dim == 256 ? attn::paged_decode_kernel<256> : attn::paged_decode_kernel<128>,
+                   dim3(attn::CTAS), dim3(attn::DECODE_THREADS),
+                   cache->head_dim == 256 ? attn::decode_smem_bytes<256>() : attn::decode_smem_bytes<128>(), s, tm_k, tm_v, p);
+        nvfp4::host::count_launch();
+        ++sets;
     }
-    nvfp4::host::count_launch();
+    p.parts = parts[tiled ? 0 : 1];
+    const dim3 join_grid(static_cast<unsigned>(attn::CTAS * sets), static_cast<unsigned>(cdiv(p.parts.rows, attn::JOIN_ROWS)));
+    launch(cache->head_dim == 256 ? attn::paged_attention_join_kernel<256> : attn::paged_attention_join_kernel<128>,
+           join_grid, dim3(attn::JOIN_ROWS * 32), 0, s, p, parts[1]);
     nvfp4::host::count_launch();
     return launch_ok();
 }

@@ -2,7 +2,7 @@
 //
 // An item is a tile of query rows of one sequence and key head: up to
 // 128 / group tokens with all `group` query heads of the key head, so every
-// key block loaded serves all of them.  An item costs its keys plus ITEM_COST
+// key block loaded serves all of them.  An item costs its keys plus item_cost
 // (loading the queries, filling the pipeline, writing the result).  The items of the batch,
 // ordered by sequence, key head and row tile, form one line of cost; CTA c of
 // n takes the c-th n-th of it, whatever the mix of long and short sequences,
@@ -21,7 +21,6 @@ namespace attn {
 
 constexpr int KEY_BLOCK = 128;
 constexpr int ROW_TILE = 128;
-constexpr int ITEM_COST = 512;
 constexpr int CTAS = 148;   // one per SM; results do not depend on the device's own count
 
 struct SeqItems {
@@ -29,11 +28,14 @@ struct SeqItems {
     int32_t tiles;  // row tiles
     int32_t past;   // len - fresh (may be negative)
     int32_t m0;     // first row tile with keys by the formula of cost()
+    int32_t extra;  // cost of an item beside its keys
 
-    __device__ __forceinline__ void set(const Seq &seq, int tile_tokens)
+    __device__ __forceinline__ void set(const Seq &seq, const BatchView &v, int tile_tokens)
     {
         s = seq;
-        tiles = (seq.fresh + tile_tokens - 1) / tile_tokens;
+        extra = v.item_cost;
+        const bool mine = seq.fresh >= v.fresh_min && seq.fresh <= v.fresh_max;
+        tiles = mine ? (seq.fresh + tile_tokens - 1) / tile_tokens : 0;
         past = seq.len - seq.fresh;
         m0 = past >= 0 ? 0 : -past / tile_tokens;
     }
@@ -41,11 +43,11 @@ struct SeqItems {
     // Cost of row tile m, and of all row tiles before m.
     __device__ __forceinline__ int64_t cost(int m, int tile_tokens) const
     {
-        return ITEM_COST + max(static_cast<int64_t>(past) + static_cast<int64_t>(tile_tokens) * (m + 1), int64_t(0));
+        return extra + max(static_cast<int64_t>(past) + static_cast<int64_t>(tile_tokens) * (m + 1), int64_t(0));
     }
     __device__ __forceinline__ int64_t before(int m, int tile_tokens) const
     {
-        int64_t sum = static_cast<int64_t>(ITEM_COST) * m;
+        int64_t sum = static_cast<int64_t>(extra) * m;
         if (m > m0) {
             const int64_t n = m - m0;
             sum += n * past + tile_tokens * (n * m0 + n * (n + 1) / 2);
@@ -94,7 +96,7 @@ struct Walk {
                             left = 0;
                             return it;
                         }
-                        q.set(load_seq(v, b, ignored), tile_tokens);
+                        q.set(load_seq(v, b, ignored), v, tile_tokens);
                     } while (q.tiles == 0);
                 }
             }
@@ -147,7 +149,7 @@ __device__ __forceinline__ void find_start(const BatchView &v, int kv_heads, int
     int64_t mine = 0;
     for (int b = b0; b < b1; ++b) {
         SeqItems q;
-        q.set(load_seq(v, b, bad), tile_tokens);
+        q.set(load_seq(v, b, bad), v, tile_tokens);
         mine += q.total(tile_tokens) * kv_heads;
     }
     int64_t scan = mine;
@@ -174,7 +176,7 @@ __device__ __forceinline__ void find_start(const BatchView &v, int kv_heads, int
     if (to > from && from >= at && from < at + mine) {
         for (int b = b0; b < b1; ++b) {
             SeqItems q;
-            q.set(load_seq(v, b, bad), tile_tokens);
+            q.set(load_seq(v, b, bad), v, tile_tokens);
             const int64_t one = q.total(tile_tokens);
             if (from < at + one * kv_heads) {
                 int64_t off = from - at;

@@ -102,6 +102,13 @@ struct PartInfo {
     int32_t pad;
 };
 
+struct Parts {
+    PartInfo *info;  // [CTAS]
+    float *o;        // [CTAS][2][rows][D]
+    float *ml;       // [CTAS][2][rows][2]: reference, sum
+    int32_t rows;
+};
+
 struct AttnParams {
     HeadRows q, gate, out;    // gate.data null: no gate
     const float *k_scale, *v_scale;
@@ -110,10 +117,7 @@ struct AttnParams {
     BatchView batch;
     // place of the page's row, head and page coordinate in the tensor maps (1..3)
     int32_t k_row_at, k_head_at, v_row_at, v_head_at;
-    PartInfo *parts;          // [CTAS]
-    float *part_o;            // [CTAS][2][part_rows][D]
-    float *part_ml;           // [CTAS][2][part_rows][2]: r, sum
-    int32_t part_rows;
+    Parts parts;
     uint32_t group_inv;       // ceil(2^16 / group): row / group = row * group_inv >> 16 for rows below 128
     uint32_t *out_amax;
     uint32_t *status;
@@ -185,29 +189,23 @@ __device__ __forceinline__ float block_max64(const uint32_t (&v)[64])
     return max3(m[0], m[1], fmaxf(m[2], m[3]));
 }
 
-// One bf16 query row (8 elements of each lane, D / 8 lanes) as two E4M3 terms.
-template <int D>
-__device__ __forceinline__ void split_query(const uint4 &v, uint2 &hi, uint2 &lo, float &unscale)
+// Scale of a query row whose largest element has the magnitude bits `mag`: the
+// power of two that puts it in [128, 256), and its inverse; NaN for a row that
+// is not finite.
+__device__ __forceinline__ void query_scale(uint32_t mag, float &scale, float &unscale)
+{
+    const int e = static_cast<int>(mag >> 7);  // exponent field: scale by 2^(134 - e), at most 2^127
+    const int up = min(134 - e, 127);
+    scale = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
+    unscale = e == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+}
+
+// Eight scaled query elements as two E4M3 terms.  A scaled value is exact in
+// f16 (8 bits; below 2^-14 it is far under the low term's step), and so is x -
+// high.
+__device__ __forceinline__ void split8(const uint4 &v, float scale, uint2 &hi, uint2 &lo)
 {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t mag = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        mag = __vmaxu2(mag, w[i] & 0x7FFF7FFFu);
-    mag = max(mag & 0xFFFFu, mag >> 16);
-    if (D == 256) {
-        mag = __reduce_max_sync(0xFFFFFFFFu, mag);
-    } else {
-#pragma unroll
-        for (int o = D / 16; o > 0; o >>= 1)
-            mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, o));
-    }
-    // exponent field e of the largest: scale by 2^(134 - e); at most 2^127
-    const int e = static_cast<int>(mag >> 7);
-    const int up = min(134 - e, 127);
-    const float scale = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
-    unscale = e == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
-    // a scaled value is exact in f16 (8 bits; below 2^-14 it is far under the low term's step), and so is x - high
     uint32_t h[4], l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -217,6 +215,61 @@ __device__ __forceinline__ void split_query(const uint4 &v, uint2 &hi, uint2 &lo
     }
     hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
     lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+}
+
+// One bf16 query row (8 elements of each lane, D / 8 lanes) as two E4M3 terms.
+template <int D>
+__device__ __forceinline__ void split_query(const uint4 &v, uint2 &hi, uint2 &lo, float &unscale)
+{
+    uint32_t mag = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+    mag = max(mag & 0xFFFFu, mag >> 16);
+    if (D == 256) {
+        mag = __reduce_max_sync(0xFFFFFFFFu, mag);
+    } else {
+#pragma unroll
+        for (int o = D / 16; o > 0; o >>= 1)
+            mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, o));
+    }
+    float scale;
+    query_scale(mag, scale, unscale);
+    split8(v, scale, hi, lo);
+}
+
+// Four columns of an output row: sums times inv (zeros where the row saw no
+// key), the gate, bf16.  Returns the running max|out| (two bf16 magnitudes).
+__device__ __forceinline__ uint32_t write_row4(const AttnParams &p, const float (&o)[4], float inv, bool empty, int32_t token,
+                                               int32_t head, int col, uint32_t amax)
+{
+    float y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        y[e] = empty ? 0.0f : o[e] * inv;
+    if (p.gate.data != nullptr) {
+        const uint2 gw = *reinterpret_cast<const uint2 *>(p.gate.data + token * p.gate.token_stride +
+                                                          head * p.gate.head_stride + col);
+        const float gx[4] = {__uint_as_float(gw.x << 16), __uint_as_float(gw.x & 0xFFFF0000u),
+                             __uint_as_float(gw.y << 16), __uint_as_float(gw.y & 0xFFFF0000u)};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            y[e] = __fdividef(y[e], 1.0f + __expf(-gx[e]));
+    }
+    const __nv_bfloat162 b0 = __floats2bfloat162_rn(y[0], y[1]), b1 = __floats2bfloat162_rn(y[2], y[3]);
+    const uint2 w = make_uint2(*reinterpret_cast<const uint32_t *>(&b0), *reinterpret_cast<const uint32_t *>(&b1));
+    *reinterpret_cast<uint2 *>(const_cast<uint16_t *>(p.out.data) + token * p.out.token_stride + head * p.out.head_stride + col) = w;
+    return __vmaxu2(__vmaxu2(amax, w.x & 0x7FFF7FFFu), w.y & 0x7FFF7FFFu);
+}
+
+// A warp's max|out| into the caller's word.
+__device__ __forceinline__ void store_amax(const AttnParams &p, uint32_t amax, int lane)
+{
+    if (p.out_amax == nullptr)
+        return;
+    amax = max(amax & 0xFFFFu, amax >> 16);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+    if (lane == 0 && amax != 0)
+        atomicMax(p.out_amax, amax);
 }
 
 template <int D>
@@ -467,7 +520,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
         walk.left = sm->start.left;
         if (walk.left > 0) {
             bool ignored = false;
-            walk.q.set(load_seq(p.batch, walk.b, ignored), p.tile_tokens);
+            walk.q.set(load_seq(p.batch, walk.b, ignored), p.batch, p.tile_tokens);
         }
         PartInfo info;
         info.continues = info.owns = 0;
@@ -516,7 +569,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
         if (lane == 0) {
             if (fail)
                 attn_timeout(sm, p.status);
-            p.parts[cta] = info;
+            p.parts.info[cta] = info;
         }
     } else if (warp >= ROW_WARP0 && warp < SOFT_WARP0) {
         // ------------------------------------------- rows: rescaling, results
@@ -622,7 +675,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
                 // The accumulator has a row per lane; memory wants a row's columns together: 32 columns at a
                 // time pass through shared memory, and 4 lanes take a row's 8 columns each.
                 const int sub = lane >> 2, c8 = (lane & 3) * 8;
-                const int64_t prow0 = (static_cast<int64_t>(cta) * 2 + (it.part == 2 ? 1 : 0)) * p.part_rows;
+                const int64_t prow0 = (static_cast<int64_t>(cta) * 2 + (it.part == 2 ? 1 : 0)) * p.parts.rows;
                 int64_t out_at[4], gate_at[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -679,7 +732,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
                             amax = __vmaxu2(__vmaxu2(amax, w.x & 0x7FFF7FFFu), w.y & 0x7FFF7FFFu);
                             amax = __vmaxu2(__vmaxu2(amax, w.z & 0x7FFF7FFFu), w.w & 0x7FFF7FFFu);
                         } else {
-                            float4 *op = reinterpret_cast<float4 *>(p.part_o + out_at[e] + col);
+                            float4 *op = reinterpret_cast<float4 *>(p.parts.o + out_at[e] + col);
                             op[0] = a;
                             op[1] = b;
                         }
@@ -687,8 +740,8 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
                     __syncwarp();
                 }
                 if (!whole && live) {
-                    p.part_ml[(prow0 + row) * 2] = sm->ref[ip][row];
-                    p.part_ml[(prow0 + row) * 2 + 1] = total;
+                    p.parts.ml[(prow0 + row) * 2] = sm->ref[ip][row];
+                    p.parts.ml[(prow0 + row) * 2 + 1] = total;
                 }
             }
             tc_fence_before();
@@ -708,14 +761,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
         }
         if (fail && lane == 0)
             attn_timeout(sm, p.status);
-        if (p.out_amax != nullptr) {
-            amax = max(amax & 0xFFFFu, amax >> 16);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-            if (lane == 0 && amax != 0)
-                atomicMax(p.out_amax, amax);
-        }
+        store_amax(p, amax, lane);
     } else if (warp >= SOFT_WARP0) {
         // ------------------------------------------------------ softmax
         const int quarter = warp & 3, half = (warp - SOFT_WARP0) >> 2, sw = warp - SOFT_WARP0;
@@ -901,26 +947,29 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
 
 // Joins the parts of the items that several CTAs worked on: CTA c's last
 // item, whose later parts are the first items of CTAs c+1 .. last.  One warp
-// per row; the parts are added in the order of their keys.
+// per row; the parts are added in the order of their keys.  A second set of
+// parts (of the kernel for single tokens beside this one's) follows the first
+// in the grid.
 constexpr int JOIN_ROWS = 8;
 
 template <int D>
-__global__ void __launch_bounds__(JOIN_ROWS * 32) paged_attention_join_kernel(const AttnParams p)
+__global__ void __launch_bounds__(JOIN_ROWS * 32) paged_attention_join_kernel(const AttnParams p, const Parts second)
 {
     grid_dep_wait();
     grid_dep_launch_dependents();
-    const int cta = blockIdx.x, lane = threadIdx.x & 31;
+    const Parts parts = blockIdx.x < CTAS ? p.parts : second;
+    const int cta = blockIdx.x % CTAS, lane = threadIdx.x & 31;
     const int row = blockIdx.y * JOIN_ROWS + (threadIdx.x >> 5);
-    const PartInfo info = p.parts[cta];
+    const PartInfo info = parts.info[cta];
     const float ks = __ldg(p.k_scale), vs = __ldg(p.v_scale);
     if (!info.owns || row >= info.rows || !valid_scale(ks) || !valid_scale(vs))
         return;
-    auto slot_of = [&](int c) { return (static_cast<int64_t>(c) * 2 + (c == cta ? 1 : 0)) * p.part_rows + row; };
-    auto has = [&](int c) { return c == cta || p.parts[c].continues != 0; };
+    auto slot_of = [&](int c) { return (static_cast<int64_t>(c) * 2 + (c == cta ? 1 : 0)) * parts.rows + row; };
+    auto has = [&](int c) { return c == cta || parts.info[c].continues != 0; };
     float top = -INFINITY;
     for (int c = cta; c <= info.last; ++c)
         if (has(c))
-            top = fmaxf(top, p.part_ml[slot_of(c) * 2]);
+            top = fmaxf(top, parts.ml[slot_of(c) * 2]);
     constexpr int PER = D / 32;
     float o[PER], sum = 0.0f;
 #pragma unroll
@@ -931,11 +980,11 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32) paged_attention_join_kernel(co
             continue;
         const int64_t s = slot_of(c);
         // no key in sight in any part: weight 1 keeps the zero or NaN sums
-        const float w = top > -INFINITY ? exp2_fast(p.part_ml[s * 2] - top) : 1.0f;
-        sum = fmaf(w, p.part_ml[s * 2 + 1], sum);
+        const float w = top > -INFINITY ? exp2_fast(parts.ml[s * 2] - top) : 1.0f;
+        sum = fmaf(w, parts.ml[s * 2 + 1], sum);
 #pragma unroll
         for (int i = 0; i < PER / 4; ++i) {
-            const float4 x = *reinterpret_cast<const float4 *>(p.part_o + s * D + i * 128 + lane * 4);
+            const float4 x = *reinterpret_cast<const float4 *>(parts.o + s * D + i * 128 + lane * 4);
             o[4 * i] = fmaf(w, x.x, o[4 * i]);
             o[4 * i + 1] = fmaf(w, x.y, o[4 * i + 1]);
             o[4 * i + 2] = fmaf(w, x.z, o[4 * i + 2]);
@@ -943,39 +992,14 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32) paged_attention_join_kernel(co
         }
     }
     const int tk = row / p.group, h = info.group0 + row - tk * p.group;
-    const bool empty = info.past0 + tk < 0;
     const float inv = vs / sum;
     uint32_t amax = 0;
 #pragma unroll
     for (int i = 0; i < PER / 4; ++i) {
-        const int col = i * 128 + lane * 4;
-        float y[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            y[e] = empty ? 0.0f : o[4 * i + e] * inv;
-        if (p.gate.data != nullptr) {
-            const uint2 gw = *reinterpret_cast<const uint2 *>(p.gate.data + (info.token0 + tk) * p.gate.token_stride +
-                                                              h * p.gate.head_stride + col);
-            const float gx[4] = {__uint_as_float(gw.x << 16), __uint_as_float(gw.x & 0xFFFF0000u),
-                                 __uint_as_float(gw.y << 16), __uint_as_float(gw.y & 0xFFFF0000u)};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                y[e] = __fdividef(y[e], 1.0f + __expf(-gx[e]));
-        }
-        const __nv_bfloat162 b0 = __floats2bfloat162_rn(y[0], y[1]), b1 = __floats2bfloat162_rn(y[2], y[3]);
-        const uint2 w = make_uint2(*reinterpret_cast<const uint32_t *>(&b0), *reinterpret_cast<const uint32_t *>(&b1));
-        *reinterpret_cast<uint2 *>(const_cast<uint16_t *>(p.out.data) + (info.token0 + tk) * p.out.token_stride +
-                                   h * p.out.head_stride + col) = w;
-        amax = __vmaxu2(__vmaxu2(amax, w.x & 0x7FFF7FFFu), w.y & 0x7FFF7FFFu);
+        const float y[4] = {o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]};
+        amax = write_row4(p, y, inv, info.past0 + tk < 0, info.token0 + tk, h, i * 128 + lane * 4, amax);
     }
-    if (p.out_amax != nullptr) {
-        amax = max(amax & 0xFFFFu, amax >> 16);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1)
-            amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
-        if (lane == 0 && amax != 0)
-            atomicMax(p.out_amax, amax);
-    }
+    store_amax(p, amax, lane);
 }
 
 }  // namespace attn

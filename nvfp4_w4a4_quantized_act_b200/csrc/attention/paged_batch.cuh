@@ -20,6 +20,10 @@ struct BatchView {
     int32_t page_shift;  // page_size = 1 << page_shift
     int32_t tokens;      // token rows of the call
     int64_t num_pages;
+    // how a kernel shares the batch (attention_schedule.cuh): the sequences it takes, by their new tokens, and what
+    // an item costs beside its keys
+    int32_t fresh_min, fresh_max;
+    int32_t item_cost;
 };
 
 // One sequence: rows [first, first + fresh) of the call, `len` cached

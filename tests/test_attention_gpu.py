@@ -56,6 +56,19 @@ def test_head_layouts(heads, kv, D):
     _run(c, heads, gated=heads % 2 == 0)
 
 
+@pytest.mark.parametrize("pad", [0, 3, 40])
+@pytest.mark.parametrize("heads,kv,D", [(1, 1, 128), (8, 1, 128), (5, 1, 256), (16, 2, 256), (21, 3, 128), (7, 7, 256), (18, 2, 128)])
+def test_decode_batches(heads, kv, D, pad):
+    """One new token each, unpadded and padded; beside them a sequence with
+    none and, where the batch has no more rows than sequences, one with two."""
+    seqs = [(1, n) for n in (1, 31, 32, 33, 64, 127, 128, 129, 500, 1025, 0)] + [(0, 77)]
+    if pad == 0:
+        seqs.append((2, 70))
+    c = Cache(seqs, kv, D, 32, seed=heads, tokens_pad=pad)
+    fill_normal(c, heads)
+    _run(c, heads)
+
+
 RAGGED = [(3, 3), (0, 40), (1, 200), (70, 70), (0, 0), (5, 130), (1, 1), (17, 333), (1, 128), (2, 129)]
 
 
@@ -120,6 +133,19 @@ def test_keys_out_of_sight_do_not_matter():
     assert torch.isfinite(out[:30].float()).all() and torch.isfinite(out[60:].float()).all()
 
 
+def test_single_token_with_nan_in_sight():
+    """A single token sees every key: NaN in a key makes its heads NaN, in a
+    value one dimension."""
+    c = Cache([(1, 200), (1, 130), (1, 40)], 2, 256, 16, seed=15)
+    fill_normal(c, 5)
+    at = c.slots(0)
+    c.k_pages[at[0][180], at[1][180], 0] = 0x7F
+    at = c.slots(1)
+    c.v_pages[at[0][129], at[1][129], 1, 37] = 0xFF
+    out = _run(c, 4, gated=False)
+    assert torch.isnan(out[0, :2].float()).all() and int(torch.isnan(out.float()).sum()) == 2 * 256 + 2
+
+
 def test_queries_that_are_not_finite():
     c = Cache([(4, 40), (1, 300)], 1, 128, 16, seed=17)
     fill_normal(c, 5)
@@ -137,6 +163,17 @@ def test_flat_and_sharp_scores(std, k_std):
     c = Cache([(1, 3000), (40, 900)], 2, 256, 64, seed=19)
     fill_normal(c, 7, k_std=k_std)
     _run(c, 8, std=std)
+
+
+def test_single_token_queries_that_are_not_finite():
+    c = Cache([(1, 300), (1, 40)], 1, 128, 16, seed=18)
+    fill_normal(c, 5)
+    q, _ = _queries(c, 3, 1)
+    q = q.clone()
+    q[0, 0, 5], q[1, 2, 6] = float("nan"), float("-inf")
+    out = ops.fp8_kv_attention(q, *c.args())
+    bad = torch.isnan(out).all(-1)
+    assert bool(bad[0, 0]) and bool(bad[1, 2]) and int(torch.isnan(out).any(-1).sum()) == 2
 
 
 @pytest.mark.parametrize("place", [0, 5, 1500, 2999])
