@@ -152,11 +152,10 @@ attn::BatchView batch_view(const nvfp4_kv_batch *b, const nvfp4_kv_pages *c, int
 
 // The pages of K or V as a 4-D byte tensor, dimensions in the order of their
 // strides behind the contiguous head_dim; row_at and head_at say where the
-// page's rows and the heads ended up.  A box is one page's rows (box_rows at most)
+// page's rows and the heads ended up.  A box is one page's rows (128 at most)
 // by 128 bytes of one head.
 int make_page_map(const nvfp4::host::Device &d, CUtensorMap *map, const void *base, const nvfp4_kv_pages *c,
-                  int64_t page_stride, int64_t row_stride, int64_t head_stride, int32_t box_rows, int32_t *row_at,
-                  int32_t *head_at)
+                  int64_t page_stride, int64_t row_stride, int64_t head_stride, int32_t *row_at, int32_t *head_at)
 {
     struct Dim {
         int64_t stride, size;
@@ -172,7 +171,7 @@ int make_page_map(const nvfp4::host::Device &d, CUtensorMap *map, const void *ba
         size[i + 1] = static_cast<cuuint64_t>(dims[i].size);
         stride[i] = static_cast<cuuint64_t>(dims[i].stride);
         if (dims[i].which == 0) {
-            box[i + 1] = static_cast<cuuint32_t>(std::min(c->page_size, box_rows));
+            box[i + 1] = static_cast<cuuint32_t>(std::min(c->page_size, attn::KEY_BLOCK));
             *row_at = i + 1;
         } else if (dims[i].which == 1) {
             *head_at = i + 1;
@@ -441,17 +440,16 @@ extern "C" int nvfp4_fp8_kv_attention(const nvfp4_heads *q, const nvfp4_heads *g
         parts_at(base + parts_bytes(part_rows(tokens, group), cache->head_dim), group)};
     if (allow_smem(d.index) != NVFP4_OK)
         return NVFP4_ERR_CUDA;
+    CUtensorMap tm_k, tm_v;
+    if (make_page_map(d, &tm_k, cache->k_pages, cache, cache->k_page_stride, cache->k_token_stride, cache->k_head_stride,
+                      &p.k_row_at, &p.k_head_at) != NVFP4_OK ||
+        make_page_map(d, &tm_v, cache->v_pages, cache, cache->v_page_stride, cache->v_token_stride, cache->v_head_stride,
+                      &p.v_row_at, &p.v_head_at) != NVFP4_OK)
+        return NVFP4_ERR_CUDA;
     int sets = 0;
     for (int k = 0; k < 2; ++k) {
         if (!(k == 0 ? tiled : single))
             continue;
-        CUtensorMap tm_k, tm_v;
-        const int32_t box_rows = k == 0 ? attn::KEY_BLOCK : attn::WARP_KEYS;
-        if (make_page_map(d, &tm_k, cache->k_pages, cache, cache->k_page_stride, cache->k_token_stride,
-                          cache->k_head_stride, box_rows, &p.k_row_at, &p.k_head_at) != NVFP4_OK ||
-            make_page_map(d, &tm_v, cache->v_pages, cache, cache->v_page_stride, cache->v_token_stride,
-                          cache->v_head_stride, box_rows, &p.v_row_at, &p.v_head_at) != NVFP4_OK)
-            return NVFP4_ERR_CUDA;
         p.parts = parts[k];
         p.tile_tokens = k == 0 ? attn::ROW_TILE / p.group : 1;
         p.batch.fresh_min = k == 0 && single ? 2 : 1;

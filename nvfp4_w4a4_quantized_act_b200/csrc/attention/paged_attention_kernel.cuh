@@ -964,31 +964,49 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32) paged_attention_join_kernel(co
     const float ks = __ldg(p.k_scale), vs = __ldg(p.v_scale);
     if (!info.owns || row >= info.rows || !valid_scale(ks) || !valid_scale(vs))
         return;
+    // A lane for every CTA of a span of 32: which hold a part, and their references and sums, all loads at once
     auto slot_of = [&](int c) { return (static_cast<int64_t>(c) * 2 + (c == cta ? 1 : 0)) * parts.rows + row; };
-    auto has = [&](int c) { return c == cta || parts.info[c].continues != 0; };
+    auto state = [&](int c, float2 &ml) {
+        const bool in = c <= info.last;
+        const bool has = in && (c == cta || parts.info[c].continues != 0);
+        ml = make_float2(-INFINITY, 0.0f);
+        if (in)
+            ml = *reinterpret_cast<const float2 *>(parts.ml + slot_of(c) * 2);
+        return has;
+    };
     float top = -INFINITY;
-    for (int c = cta; c <= info.last; ++c)
-        if (has(c))
-            top = fmaxf(top, parts.ml[slot_of(c) * 2]);
+    for (int c = cta + lane; c - lane <= info.last; c += 32) {
+        float2 ml;
+        if (state(c, ml))
+            top = fmaxf(top, ml.x);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
     constexpr int PER = D / 32;
     float o[PER], sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < PER; ++i)
         o[i] = 0.0f;
-    for (int c = cta; c <= info.last; ++c) {
-        if (!has(c))
-            continue;
-        const int64_t s = slot_of(c);
+    for (int c0 = cta; c0 <= info.last; c0 += 32) {
+        float2 ml;
+        uint32_t todo = __ballot_sync(0xFFFFFFFFu, state(c0 + lane, ml));
         // no key in sight in any part: weight 1 keeps the zero or NaN sums
-        const float w = top > -INFINITY ? exp2_fast(parts.ml[s * 2] - top) : 1.0f;
-        sum = fmaf(w, parts.ml[s * 2 + 1], sum);
+        const float mine = top > -INFINITY ? exp2_fast(ml.x - top) : 1.0f;
+        while (todo) {
+            const int k = __ffs(todo) - 1;
+            todo &= todo - 1;
+            const float w = __shfl_sync(0xFFFFFFFFu, mine, k);
+            sum = fmaf(w, __shfl_sync(0xFFFFFFFFu, ml.y, k), sum);
+            const float *src = parts.o + slot_of(c0 + k) * D + lane * 4;
 #pragma unroll
-        for (int i = 0; i < PER / 4; ++i) {
-            const float4 x = *reinterpret_cast<const float4 *>(parts.o + s * D + i * 128 + lane * 4);
-            o[4 * i] = fmaf(w, x.x, o[4 * i]);
-            o[4 * i + 1] = fmaf(w, x.y, o[4 * i + 1]);
-            o[4 * i + 2] = fmaf(w, x.z, o[4 * i + 2]);
-            o[4 * i + 3] = fmaf(w, x.w, o[4 * i + 3]);
+            for (int i = 0; i < PER / 4; ++i) {
+                const float4 x = *reinterpret_cast<const float4 *>(src + i * 128);
+                o[4 * i] = fmaf(w, x.x, o[4 * i]);
+                o[4 * i + 1] = fmaf(w, x.y, o[4 * i + 1]);
+                o[4 * i + 2] = fmaf(w, x.z, o[4 * i + 2]);
+                o[4 * i + 3] = fmaf(w, x.w, o[4 * i + 3]);
+            }
         }
     }
     const int tk = row / p.group, h = info.group0 + row - tk * p.group;
