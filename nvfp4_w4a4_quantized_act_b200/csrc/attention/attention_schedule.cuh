@@ -73,6 +73,16 @@ struct Item {
 
 // A CTA's walk over its part of the line.
 struct Walk {
+    // Key block that a boundary at cost x of an item of cost c falls to.  In
+    // fp64 for large items: rounded, but alike for both neighbours of the
+    // boundary and never falling as x grows.
+    static __device__ __forceinline__ int block_at(int64_t x, int blocks, int64_t c)
+    {
+        if (c < (1 << 20) && blocks < (1 << 12))
+            return static_cast<int>(static_cast<uint32_t>(x) * static_cast<uint32_t>(blocks) / static_cast<uint32_t>(c));
+        return static_cast<int>(static_cast<double>(x) * blocks / static_cast<double>(c));
+    }
+
     int b, h, m;
     int64_t x;     // offset in the item
     int64_t left;  // cost left
@@ -106,9 +116,8 @@ struct Walk {
             const int tokens = min(q.s.fresh - first, tile_tokens);
             it.keys = max(q.past + first + tokens, 0);
             const int blocks = max((it.keys + KEY_BLOCK - 1) / KEY_BLOCK, 1);
-            // in fp64: rounded, but alike for both neighbours of a boundary and never falling as x grows
-            const int t0 = static_cast<int>(static_cast<double>(x) * blocks / static_cast<double>(c));
-            const int t1 = x1 == c ? blocks : static_cast<int>(static_cast<double>(x1) * blocks / static_cast<double>(c));
+            const int t0 = x == 0 ? 0 : block_at(x, blocks, c);
+            const int t1 = x1 == c ? blocks : block_at(x1, blocks, c);
             end_cost = c - x1;
             left -= x1 - x;
             it.t0 = t0;
@@ -181,7 +190,8 @@ __device__ __forceinline__ void find_start(const BatchView &v, int kv_heads, int
             if (from < at + one * kv_heads) {
                 int64_t off = from - at;
                 st->b = b;
-                st->h = static_cast<int>(off / one);
+                st->h = (off | one) >> 32 ? static_cast<int>(off / one)
+                                          : static_cast<int>(static_cast<uint32_t>(off) / static_cast<uint32_t>(one));
                 off -= st->h * one;
                 int lo = 0, hi = q.tiles - 1;  // last row tile that starts at or before off
                 while (lo < hi) {

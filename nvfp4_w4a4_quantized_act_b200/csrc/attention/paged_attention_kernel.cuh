@@ -327,17 +327,28 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
 
     const float ks = __ldg(p.k_scale), vs = __ldg(p.v_scale);
     const bool scales_ok = valid_scale(ks) && valid_scale(vs);
-    bool bad = false;
-    find_start<ATTN_THREADS>(p.batch, p.kv_heads, p.tile_tokens, cta, &sm->start, sm->scratch, bad);
-    if (cta == 0) {
-        if (!scales_ok && tid == 0)
-            atomicOr(p.status, kStatusNonFinite);
-        if (bad)
-            atomicOr(p.status, kStatusBadIndex);
+    // Beside the kernel for single tokens this one may find nothing to do: a look at the offsets alone says so, and
+    // the other kernel reports what is malformed.
+    bool idle = false;
+    if (p.batch.fresh_min > 1) {
+        bool some = false;
+        for (int b = tid; b < p.batch.num_seqs; b += ATTN_THREADS)
+            some |= __ldg(p.batch.cu + b + 1) - __ldg(p.batch.cu + b) >= p.batch.fresh_min;
+        idle = __syncthreads_or(some) == 0;
     }
-    if (!scales_ok && tid == 0)
-        sm->start.left = 0;
-    __syncthreads();
+    if (!idle) {
+        bool bad = false;
+        find_start<ATTN_THREADS>(p.batch, p.kv_heads, p.tile_tokens, cta, &sm->start, sm->scratch, bad);
+        if (cta == 0) {
+            if (!scales_ok && tid == 0)
+                atomicOr(p.status, kStatusNonFinite);
+            if (bad)
+                atomicOr(p.status, kStatusBadIndex);
+        }
+        if (!scales_ok && tid == 0)
+            sm->start.left = 0;
+        __syncthreads();
+    }
 
     // The next item, from warp 2; blocks = 0 at the end or when unwinding.
     auto take_item = [&](int i, bool &fail) -> Item {
@@ -350,7 +361,13 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
         return it;
     };
 
-    if (warp == 0) {
+    if (idle) {
+        if (tid == 0) {
+            PartInfo none;
+            none.continues = none.owns = none.last = none.token0 = none.rows = none.group0 = none.past0 = none.pad = 0;
+            p.parts.info[cta] = none;
+        }
+    } else if (warp == 0) {
         // ------------------------------------------------------ loads
         const int shift = p.batch.page_shift, page = 1 << shift;
         const int rows = min(page, KEY_BLOCK);        // rows of a box
@@ -994,18 +1011,31 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32) paged_attention_join_kernel(co
         // no key in sight in any part: weight 1 keeps the zero or NaN sums
         const float mine = top > -INFINITY ? exp2_fast(ml.x - top) : 1.0f;
         while (todo) {
-            const int k = __ffs(todo) - 1;
-            todo &= todo - 1;
-            const float w = __shfl_sync(0xFFFFFFFFu, mine, k);
-            sum = fmaf(w, __shfl_sync(0xFFFFFFFFu, ml.y, k), sum);
-            const float *src = parts.o + slot_of(c0 + k) * D + lane * 4;
+            // eight parts' sums at a time
+            int k[8];
+            float4 x[8][PER / 4];
 #pragma unroll
-            for (int i = 0; i < PER / 4; ++i) {
-                const float4 x = *reinterpret_cast<const float4 *>(src + i * 128);
-                o[4 * i] = fmaf(w, x.x, o[4 * i]);
-                o[4 * i + 1] = fmaf(w, x.y, o[4 * i + 1]);
-                o[4 * i + 2] = fmaf(w, x.z, o[4 * i + 2]);
-                o[4 * i + 3] = fmaf(w, x.w, o[4 * i + 3]);
+            for (int e = 0; e < 8; ++e) {
+                k[e] = todo ? __ffs(todo) - 1 : -1;
+                todo &= todo - 1;
+                const float *src = parts.o + slot_of(c0 + max(k[e], 0)) * D + lane * 4;
+#pragma unroll
+                for (int i = 0; i < PER / 4; ++i)
+                    x[e][i] = k[e] >= 0 ? *reinterpret_cast<const float4 *>(src + i * 128) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (k[e] < 0)
+                    break;
+                const float w = __shfl_sync(0xFFFFFFFFu, mine, k[e]);
+                sum = fmaf(w, __shfl_sync(0xFFFFFFFFu, ml.y, k[e]), sum);
+#pragma unroll
+                for (int i = 0; i < PER / 4; ++i) {
+                    o[4 * i] = fmaf(w, x[e][i].x, o[4 * i]);
+                    o[4 * i + 1] = fmaf(w, x[e][i].y, o[4 * i + 1]);
+                    o[4 * i + 2] = fmaf(w, x[e][i].z, o[4 * i + 2]);
+                    o[4 * i + 3] = fmaf(w, x[e][i].w, o[4 * i + 3]);
+                }
             }
         }
     }

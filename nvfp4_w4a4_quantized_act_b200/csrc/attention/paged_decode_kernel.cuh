@@ -21,6 +21,8 @@
 //   warps 0..7   16 keys of every block of 128
 //   warp 8       walks the CTA's items (attention_schedule.cuh) and loads K and
 //                V blocks page by page (4-D TMA, 128-byte swizzle) into a ring
+//   warps 9..11  add the warps' sums of an item and write its result, while
+//                warps 0..7 are at the next item
 //
 // Fragments come straight from the stages.  K: a lane takes 16 bytes of a key
 // at a time, the operands of four MMAs (any order of the dimensions serves, the
@@ -47,7 +49,8 @@ namespace nvfp4 {
 namespace attn {
 
 constexpr int DECODE_WARPS = 8;
-constexpr int DECODE_THREADS = (DECODE_WARPS + 1) * 32;
+constexpr int WRITE_WARPS = 3;
+constexpr int DECODE_THREADS = (DECODE_WARPS + 1 + WRITE_WARPS) * 32;
 constexpr int DECODE_ROWS = 8;     // query heads of a key head, at most
 constexpr int WARP_KEYS = KEY_BLOCK / DECODE_WARPS;
 constexpr int KEY_PARTS = DECODE_WARPS / 2;   // sums of two warps that meet in shared memory
@@ -70,6 +73,7 @@ struct DecodeSmem {
     Item items[ITEMS];
     uint64_t item_ready[ITEMS], item_done[ITEMS];
     uint64_t full[DecodeShape<D>::STAGES], empty[DecodeShape<D>::STAGES];
+    uint64_t pair_ready[KEY_PARTS], o_ready, o_free;
     volatile int32_t abort_flag;
     WalkStart start;
     int64_t scratch[DECODE_THREADS / 32];
@@ -137,8 +141,12 @@ __global__ void __launch_bounds__(DECODE_THREADS, 1)
         }
         for (int i = 0; i < ITEMS; ++i) {
             mbar_init(smem_u32(&sm->item_ready[i]), 1);
-            mbar_init(smem_u32(&sm->item_done[i]), DECODE_WARPS);
+            mbar_init(smem_u32(&sm->item_done[i]), WRITE_WARPS);
         }
+        for (int i = 0; i < KEY_PARTS; ++i)
+            mbar_init(smem_u32(&sm->pair_ready[i]), 1);
+        mbar_init(smem_u32(&sm->o_ready), KEY_PARTS);
+        mbar_init(smem_u32(&sm->o_free), WRITE_WARPS);
         sm->abort_flag = 0;
         fence_mbarrier_init();
         prefetch_tensormap(&tmK);
@@ -206,6 +214,14 @@ __global__ void __launch_bounds__(DECODE_THREADS, 1)
                 info.group0 = it.head * p.group;
                 info.past0 = it.past0;
             }
+            if (lane < it.rows * (D / 64)) {  // the rows that the other warps will read
+                const int64_t h = it.head * p.group + lane / (D / 64);
+                const int col = (lane % (D / 64)) * 64;
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q.data + it.token0 * p.q.token_stride + h * p.q.head_stride + col));
+                if (p.gate.data != nullptr)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(p.gate.data + it.token0 * p.gate.token_stride +
+                                                                 h * p.gate.head_stride + col));
+            }
             const int32_t *table = p.batch.table + it.seq * p.batch.table_stride;
             const int t1 = it.t0 + it.blocks;
             auto wanted = [&](int t) { return t < t1 && lane < boxes && t * KEY_BLOCK + lane * rows < it.keys; };
@@ -258,14 +274,14 @@ __global__ void __launch_bounds__(DECODE_THREADS, 1)
         }
         if (lane == 0)
             p.parts.info[cta] = info;
-    } else {
+    } else if (warp < DECODE_WARPS) {
         // ------------------------------------------------ products, softmax
         const int g = lane >> 2, q = lane & 3;
         auto key_of = [](int n) { return (n & 1) ? ((n - 1) ^ 4) + 1 : n; };
         const int krow = key_of(g), vrow0 = key_of(2 * q), vrow1 = key_of(2 * q + 1);
         const float c = p.softmax_scale * ks * 1.4426950408889634f;
         const uint8_t *my_k = smem + warp * WARP_KEYS * 128;
-        uint32_t uses = 0, amax = 0;
+        uint32_t uses = 0;
         bool fail = false;
         for (int i = 0;; ++i) {
             Item it;
@@ -275,7 +291,7 @@ __global__ void __launch_bounds__(DECODE_THREADS, 1)
             else
                 fail = true;
             fail = __any_sync(0xFFFFFFFFu, fail);
-            if (!fail && it.blocks == 0)
+            if (fail || it.blocks == 0)
                 break;
             // Queries as the MMAs' B operands: column g, 16 dimensions at 64 s + 16 q for every s
             uint32_t qb[D / 2 / 4];
@@ -285,7 +301,7 @@ __global__ void __launch_bounds__(DECODE_THREADS, 1)
 #pragma unroll
                 for (int s = 0; s < D / 32; ++s)
                     v[s] = make_uint4(0, 0, 0, 0);
-                if (g < it.rows && !fail) {
+                if (g < it.rows) {
                     const uint16_t *src = p.q.data + it.token0 * p.q.token_stride +
                                           static_cast<int64_t>(it.head * p.group + g) * p.q.head_stride + 16 * q;
 #pragma unroll
@@ -436,6 +452,8 @@ __global__ void __launch_bounds__(DECODE_THREADS, 1)
             }
             const int part = warp % KEY_PARTS;
             float4 *frag = reinterpret_cast<float4 *>(&sm->o[part][0][0]);  // [tile][lane]
+            if (i > 0)  // the item before has been written
+                fail = fail || !mbar_wait(smem_u32(&sm->o_free), (i - 1) & 1, ATTN_WAIT_NS);
             if (warp >= KEY_PARTS) {
 #pragma unroll
                 for (int n = 0; n < A::TILES; ++n)
@@ -444,8 +462,13 @@ __global__ void __launch_bounds__(DECODE_THREADS, 1)
                     sm->ml[part][2 * q] = ml[0];
                     sm->ml[part][2 * q + 1] = ml[1];
                 }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_u32(&sm->pair_ready[part]));
+            } else {
+                fail = fail || !mbar_wait(smem_u32(&sm->pair_ready[part]), i & 1, ATTN_WAIT_NS);
             }
-            fail = named_barrier_any(1, DECODE_WARPS * 32, fail);
+            fail = __any_sync(0xFFFFFFFFu, fail);
             if (fail)
                 break;
             if (warp < KEY_PARTS) {
@@ -479,12 +502,34 @@ __global__ void __launch_bounds__(DECODE_THREADS, 1)
                     sm->ml[part][2 * q] = ml[0];
                     sm->ml[part][2 * q + 1] = ml[1];
                 }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_u32(&sm->o_ready));
             }
-            named_barrier_sync(1, DECODE_WARPS * 32);
+        }
+        if (fail && lane == 0)
+            decode_timeout(sm, p.status);
+    } else {
+        // ------------------------------------------------ results
+        uint32_t amax = 0;
+        bool fail = false;
+        for (int i = 0;; ++i) {
+            Item it;
+            it.blocks = 0;
+            if (mbar_wait(smem_u32(&sm->item_ready[i % ITEMS]), (i / ITEMS) & 1, ATTN_WAIT_NS))
+                it = sm->items[i % ITEMS];
+            else
+                fail = true;
+            fail = __any_sync(0xFFFFFFFFu, fail);
+            if (fail || it.blocks == 0)
+                break;
+            fail = __any_sync(0xFFFFFFFFu, !mbar_wait(smem_u32(&sm->o_ready), i & 1, ATTN_WAIT_NS));
+            if (fail)
+                break;
             const bool whole = it.part == 0;
             const int64_t prow0 = (static_cast<int64_t>(cta) * 2 + (it.part == 2 ? 1 : 0)) * p.parts.rows;
 #pragma unroll 1
-            for (int k = tid; k < it.rows * (D / 4); k += DECODE_WARPS * 32) {
+            for (int k = tid - (DECODE_WARPS + 1) * 32; k < it.rows * (D / 4); k += WRITE_WARPS * 32) {
                 const int r = k / (D / 4), col = (k % (D / 4)) * 4;
                 float m = -INFINITY;
 #pragma unroll
@@ -513,9 +558,10 @@ __global__ void __launch_bounds__(DECODE_THREADS, 1)
                 }
             }
             __syncwarp();
-            named_barrier_sync(1, DECODE_WARPS * 32);  // the sums are read before the next item's come
-            if (lane == 0)
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&sm->o_free));
                 mbar_arrive(smem_u32(&sm->item_done[i % ITEMS]));
+            }
         }
         if (fail && lane == 0)
             decode_timeout(sm, p.status);
