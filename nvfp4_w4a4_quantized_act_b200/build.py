@@ -31,6 +31,32 @@ def attention_sources() -> list[str]:
     return sorted(glob.glob(os.path.join(CSRC, "attention", "*.cu")))
 
 
+BINDING = os.path.join(PKG, "_attention.so")
+BINDING_SOURCE = os.path.join(CSRC, "binding", "attention_binding.cpp")
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """The CPython module that marshals the attention layer's arguments (torch
+    headers; linked to torch and Python only)."""
+    inputs = [BINDING_SOURCE, os.path.join(INCLUDE, "nvfp4.h")]
+    if not force and os.path.exists(BINDING) and all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in inputs):
+        return BINDING
+    import sysconfig
+    import torch
+    from torch.utils import cpp_extension
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-I", os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"),
+           *[a for d in cpp_extension.include_paths() for a in ("-isystem", d)], BINDING_SOURCE, "-o", tmp,
+           "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.check_call(cmd)
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def deps() -> list[str]:
     headers = [f for d in (CSRC, os.path.join(CSRC, "attention")) for ext in ("*.cuh", "*.h")
                for f in sorted(glob.glob(os.path.join(d, ext)))]
@@ -45,6 +71,7 @@ def up_to_date() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
+    build_binding(force, verbose)
     if not force and up_to_date():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"

@@ -8,9 +8,8 @@ library is missing or the device is not an sm_100 GPU, every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
-import struct
-import threading
 from dataclasses import dataclass
 
 import torch
@@ -538,139 +537,36 @@ def fp8_kv_quantize(X: torch.Tensor, scale: torch.Tensor, out=None, stream=None)
 # ------------------------------------- attention over the paged FP8 KV cache
 #
 # A decode step makes these calls for every attention layer, and a small one
-# takes the GPU no longer than the host: so the checks read each tensor
-# property once, and the host structs are packed into a buffer that each
-# thread keeps (the library reads them before the call returns).
+# takes the GPU a few microseconds: their arguments are checked and packed by
+# a CPython module (csrc/binding), which raises ValueError where the other
+# calls' checks here do.
 
-_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
-_HEADS_FMT, _PAGES_FMT, _BATCH_FMT, _NORM_FMT, _OPTS_FMT = "Qqqq", "QQQQqqqqqqqiii4x", "QQQqii", "QQQifI4x", "fI"
-_PACK_NORM = struct.Struct("=" + 4 * _HEADS_FMT + _NORM_FMT)
-_PACK_APPEND = struct.Struct("=" + 2 * _HEADS_FMT + _PAGES_FMT + _BATCH_FMT + _NORM_FMT)
-_PACK_ATTEND = struct.Struct("=" + 3 * _HEADS_FMT + _PAGES_FMT + _BATCH_FMT + _OPTS_FMT)
-_NO_HEADS = (0, 0, 0, 0)
-_tls = threading.local()
+BINDING_PATH = os.path.join(_PKG, "_attention.so")
+_native = None
 
 
-def _scratch():
-    """This thread's buffer for host structs, and its address."""
-    try:
-        return _tls.structs
-    except AttributeError:
-        buf = ctypes.create_string_buffer(512)
-        _tls.structs = buf, ctypes.addressof(buf)
-        return _tls.structs
+def _attention():
+    """The marshalling module, bound to the library (raises if it has not been
+    built)."""
+    global _native
+    if _native is None:
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"{BINDING_PATH} is missing: build it with nvfp4_w4a4_quantized_act_b200.build.build()")
+        spec = importlib.util.spec_from_file_location("_attention", BINDING_PATH)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        L = lib()
+        m.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                 for f in (L.nvfp4_qk_norm_rope, L.nvfp4_fp8_kv_append, L.nvfp4_fp8_kv_attention,
+                           L.nvfp4_fp8_kv_attention_workspace_bytes)), False)
+        _native = m
+    return _native
 
 
-def _device_of(t):
-    """Index of the current device, on which the tensor has to be (the library
-    launches there)."""
-    _require_cuda(t)
-    dev = t.get_device()
-    if dev != torch._C._cuda_getDevice():
-        raise ValueError(f"tensors on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
-    return dev
-
-
-def _stream_ptr(stream, dev):
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-
-
-def _elsewhere(t, dev, name):
-    _require_cuda(t)
-    raise ValueError(f"{name} is on {t.device}, the other tensors on device {dev}")
-
-
-def _heads(t, name, dev, like=None, written=False):
-    """nvfp4_heads of a bf16 [tokens, heads, head_dim] tensor or view; `like`:
-    the shape it must have; `written`: no two of its rows may overlap."""
-    shape, st = t.shape, t.stride()
-    if t.dtype is not _BF16 or len(shape) != 3 or st[2] != 1:
-        raise ValueError(f"{name} must be a bf16 [tokens, heads, head_dim] tensor with unit stride along head_dim "
-                         f"(got {t.dtype}, shape {tuple(shape)}, strides {st})")
-    if like is not None and shape != like:
-        raise ValueError(f"{name} has shape {tuple(shape)}, expected {tuple(like)}")
-    if t.get_device() != dev:
-        _elsewhere(t, dev, name)
-    T, H, D = shape
-    s0, s1 = st[0] if T > 1 else 0, st[1] if H > 1 else 0
-    if written and not ((H <= 1 or s1 >= D) and (T <= 1 or s0 >= (H - 1) * s1 + D)) and \
-            not ((T <= 1 or s0 >= D) and (H <= 1 or s1 >= (T - 1) * s0 + D)):
-        raise ValueError(f"{name}'s rows overlap (shape {tuple(shape)}, strides {st})")
-    return t.data_ptr(), s0, s1, H
-
-
-def _vector(t, name, dtype, n, dev):
-    """Address of a contiguous vector of at least n elements (None: null)."""
-    if t is None:
-        return 0
-    shape = t.shape
-    if t.dtype is not dtype or len(shape) != 1 or shape[0] < n or (shape[0] > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be a contiguous {dtype} vector of at least {n} (got {t.dtype}, "
-                         f"shape {tuple(shape)}, strides {t.stride()})")
-    if t.get_device() != dev:
-        _elsewhere(t, dev, name)
-    return t.data_ptr()
-
-
-def _scalar(t, name, dev):
-    if t.dtype is not _F32 or t.numel() != 1:
-        raise ValueError(f"{name} must hold one fp32 value")
-    if t.get_device() != dev:
-        _elsewhere(t, dev, name)
-    return t.data_ptr()
-
-
-def _norm_rope(head_dim, inv_freq, q_weight, k_weight, eps, plus_one, dev):
-    """Fields of nvfp4_norm_rope."""
-    for w in (q_weight, k_weight):
-        if w is not None and w.shape[0] != head_dim:
-            raise ValueError(f"a norm weight must be a bf16 [{head_dim}] tensor (got shape {tuple(w.shape)})")
-    return (_vector(q_weight, "q_weight", _BF16, head_dim, dev), _vector(k_weight, "k_weight", _BF16, head_dim, dev),
-            _vector(inv_freq, "inv_freq", _F32, 0, dev), 0 if inv_freq is None else 2 * inv_freq.shape[0], eps,
-            NVFP4_NORM_PLUS_ONE if plus_one else 0)
-
-
-def _page_strides(shape, st):
-    """Byte strides of pages, rows and heads; a dimension of one element gets
-    a stride that nests with the others (torch leaves it arbitrary)."""
-    row = st[1]
-    head = st[2] if shape[2] > 1 else row
-    return st[0] if shape[0] > 1 else max(row * shape[1], head * shape[2]), row, head
-
-
-def _kv_pages(k_pages, v_pages, k_scale, v_scale, dev):
-    """Fields of nvfp4_kv_pages."""
-    shape, ks, vs = k_pages.shape, k_pages.stride(), v_pages.stride()
-    if k_pages.dtype is not _U8 or v_pages.dtype is not _U8 or len(shape) != 4 or v_pages.shape != shape or \
-            ks[3] != 1 or vs[3] != 1:
-        raise ValueError(f"k_pages and v_pages must be uint8 [pages, page_size, kv_heads, head_dim] tensors of one shape "
-                         f"with unit stride along head_dim (got {k_pages.dtype} {tuple(shape)} {ks}, {v_pages.dtype} "
-                         f"{tuple(v_pages.shape)} {vs})")
-    if k_pages.get_device() != dev:
-        _elsewhere(k_pages, dev, "k_pages")
-    if v_pages.get_device() != dev:
-        _elsewhere(v_pages, dev, "v_pages")
-    return (k_pages.data_ptr(), v_pages.data_ptr(), _scalar(k_scale, "k_scale", dev), _scalar(v_scale, "v_scale", dev),
-            *_page_strides(shape, ks), *_page_strides(shape, vs), *shape)
-
-
-def _kv_batch(page_table, cu_tokens, seq_lens, dev):
-    """Fields of nvfp4_kv_batch."""
-    shape = page_table.shape
-    if page_table.dtype is not _I32 or len(shape) != 2 or (shape[1] > 1 and page_table.stride(1) != 1):
-        raise ValueError(f"page_table must be an int32 [sequences, pages] tensor with unit stride along pages "
-                         f"(got {page_table.dtype}, {tuple(shape)}, {page_table.stride()})")
-    if page_table.get_device() != dev:
-        _elsewhere(page_table, dev, "page_table")
-    B, P = shape
-    return (page_table.data_ptr(), _vector(cu_tokens, "cu_tokens", _I32, B + 1, dev),
-            _vector(seq_lens, "seq_lens", _I32, B, dev), page_table.stride(0) if B > 1 else P, B, P)
-
-
-def _new(stream, *size, dtype, device):
+def _new(stream, shape, dtype, device):
     """An output or scratch tensor for a call on `stream` (None: the current
     one); the allocator must know when that is another stream."""
-    t = torch.empty(size, dtype=dtype, device=device)
+    t = torch.empty(shape, dtype=dtype, device=device)
     if stream is not None and t.is_cuda:
         t.record_stream(stream)
     return t
@@ -683,32 +579,12 @@ def qk_norm_rope(q, k, positions, inv_freq=None, q_weight=None, k_weight=None, e
     positions: int32 [tokens]; inv_freq: fp32 [rotary_dim / 2] (None: no
     rotation); weights: bf16 [head_dim] (None: no norm; plus_one: 1 + w).  An
     output may be its input."""
-    dev = _device_of(q)
-    shape = q.shape
-    hq = _heads(q, "q", dev)
-    T, _, D = shape
     if q_out is None:
-        q_out = _new(stream, *shape, dtype=_BF16, device=q.device)
-    hqo = _heads(q_out, "q_out", dev, shape, True)
-    hk = hko = _NO_HEADS
-    if k is not None:
-        hk = _heads(k, "k", dev)
-        kshape = k.shape
-        if kshape[0] != T or kshape[2] != D:
-            raise ValueError(f"k has shape {tuple(kshape)}, q {tuple(shape)}")
-        if k_out is None:
-            k_out = _new(stream, *kshape, dtype=_BF16, device=q.device)
-        hko = _heads(k_out, "k_out", dev, kshape, True)
-    elif k_out is not None:
-        raise ValueError("k_out without k")
-    if inv_freq is not None and positions is None:
-        raise ValueError("a rotation needs positions")
-    pos = _vector(positions, "positions", _I32, T, dev)
-    buf, at = _scratch()
-    _PACK_NORM.pack_into(buf, 0, *hq, *hqo, *hk, *hko,
-                         *_norm_rope(D, inv_freq, q_weight, k_weight, eps, plus_one, dev))
-    rc = lib().nvfp4_qk_norm_rope(at, at + 64 if k is not None else None, at + 32, at + 96 if k is not None else None,
-                                  T, D, pos, at + 128, _stream_ptr(stream, dev))
+        q_out = _new(stream, q.shape, torch.bfloat16, q.device)
+    if k is not None and k_out is None:
+        k_out = _new(stream, k.shape, torch.bfloat16, q.device)
+    rc = (_native or _attention()).qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, eps, plus_one, q_out, k_out,
+                                                stream)
     if rc:
         raise Nvfp4Error(rc, "nvfp4_qk_norm_rope")
     return q_out, k_out
@@ -720,17 +596,8 @@ def fp8_kv_append(k, v, k_pages, v_pages, k_scale, v_scale, page_table, cu_token
     way) and values, bf16 [tokens, kv_heads, head_dim], as E4M3 codes into the
     pages of their sequences (see nvfp4_kv_batch).  Pages: uint8 [pages,
     page_size, kv_heads, head_dim], any nested strides; scales: fp32 [1]."""
-    dev = _device_of(k)
-    shape = k.shape
-    hk, hv = _heads(k, "k", dev), _heads(v, "v", dev, shape)
-    pages = _kv_pages(k_pages, v_pages, k_scale, v_scale, dev)
-    if shape[1:] != pages[-2:]:
-        raise ValueError(f"k has shape {tuple(shape)}, the pages {tuple(k_pages.shape)}")
-    pos = _vector(positions, "positions", _I32, shape[0], dev)
-    buf, at = _scratch()
-    _PACK_APPEND.pack_into(buf, 0, *hk, *hv, *pages, *_kv_batch(page_table, cu_tokens, seq_lens, dev),
-                           *_norm_rope(shape[2], inv_freq, None, k_weight, eps, plus_one, dev))
-    rc = lib().nvfp4_fp8_kv_append(at, at + 32, shape[0], at + 64, at + 168, pos, at + 208, _stream_ptr(stream, dev))
+    rc = (_native or _attention()).fp8_kv_append(k, v, k_pages, v_pages, k_scale, v_scale, page_table, cu_tokens, seq_lens,
+                                                 inv_freq, k_weight, eps, plus_one, positions, stream)
     if rc:
         raise Nvfp4Error(rc, "nvfp4_fp8_kv_append")
 
@@ -746,36 +613,14 @@ def fp8_kv_attention(q, k_pages, v_pages, k_scale, v_scale, page_table, cu_token
     times sigmoid(gate).  softmax_scale defaults to head_dim ** -0.5; out_amax
     (4 bytes, e.g. the first word of a quantize workspace) receives max|out|
     for quantize_act(..., amax_given=True)."""
-    dev = _device_of(q)
-    shape = q.shape
-    hq = _heads(q, "q", dev)
-    T, H, D = shape
-    pages = _kv_pages(k_pages, v_pages, k_scale, v_scale, dev)
-    Hk = pages[-2]
-    if D != pages[-1] or Hk == 0 or H % Hk:
-        raise ValueError(f"q has shape {tuple(shape)}, the pages {tuple(k_pages.shape)}")
-    batch = _kv_batch(page_table, cu_tokens, seq_lens, dev)
-    hg = _NO_HEADS if gate is None else _heads(gate, "gate", dev, shape)
     if out is None:
-        out = _new(stream, T, H, D, dtype=_BF16, device=q.device)
-    ho = _heads(out, "out", dev, shape, True)
-    L = lib()
-    need = L.nvfp4_fp8_kv_attention_workspace_bytes(T, H, Hk, D)
+        out = _new(stream, q.shape, torch.bfloat16, q.device)
     if ws is None:
-        ws = _new(stream, max(need, 16), dtype=_U8, device=q.device)
-    _buffer(ws, need, "ws")
-    if ws.get_device() != dev:
-        _elsewhere(ws, dev, "ws")
-    amax = None
-    if out_amax is not None:
-        _buffer(out_amax, 4, "out_amax")
-        if out_amax.get_device() != dev:
-            _elsewhere(out_amax, dev, "out_amax")
-        amax = out_amax.data_ptr()
-    buf, at = _scratch()
-    _PACK_ATTEND.pack_into(buf, 0, *hq, *hg, *ho, *pages, *batch, D ** -0.5 if softmax_scale is None else softmax_scale, 0)
-    rc = L.nvfp4_fp8_kv_attention(at, None if gate is None else at + 32, at + 64, T, at + 96, at + 200, at + 240, amax,
-                                  ws.data_ptr(), _nbytes(ws), _stream_ptr(stream, dev))
+        need = fp8_kv_attention_workspace_bytes(q.shape[0], q.shape[1], k_pages.shape[2], q.shape[2]) \
+            if q.dim() == 3 and k_pages.dim() == 4 else 0
+        ws = _new(stream, max(need, 16), torch.uint8, q.device)
+    rc = (_native or _attention()).fp8_kv_attention(q, k_pages, v_pages, k_scale, v_scale, page_table, cu_tokens, seq_lens,
+                                                    softmax_scale, gate, out, out_amax, ws, stream)
     if rc:
         raise Nvfp4Error(rc, "nvfp4_fp8_kv_attention")
     return out

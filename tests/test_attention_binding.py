@@ -2,6 +2,7 @@
 status codes (nothing is launched, no pointer is followed) and the binding's
 ValueErrors before the library is called."""
 import ctypes
+import types
 
 import pytest
 import torch
@@ -135,22 +136,43 @@ def test_workspace_sizes():
 
 
 class _Recorder:
-    def __init__(self, real):
-        self.real, self.calls = real, []
+    """Stands in for the library: counts the calls and copies the host structs
+    that each is given."""
+    NAMES = ("nvfp4_qk_norm_rope", "nvfp4_fp8_kv_append", "nvfp4_fp8_kv_attention")
+    STRUCTS = {
+        "nvfp4_qk_norm_rope": ((0, ops.Heads), (1, ops.Heads), (2, ops.Heads), (3, ops.Heads), (7, ops.NormRope)),
+        "nvfp4_fp8_kv_append": ((0, ops.Heads), (1, ops.Heads), (3, ops.KvPages), (4, ops.KvBatch), (6, ops.NormRope)),
+        "nvfp4_fp8_kv_attention": ((0, ops.Heads), (1, ops.Heads), (2, ops.Heads), (4, ops.KvPages), (5, ops.KvBatch),
+                                   (6, ops.AttentionOpts)),
+    }
 
-    def __getattr__(self, name):
-        if name.endswith("_bytes"):
-            return getattr(self.real, name)
-        return lambda *a: self.calls.append(name) or 0
+    def __init__(self):
+        self.calls, self.args, self.structs, self.status = [], {}, {}, 0
+        self.keep = [self._callback(n) for n in self.NAMES]
+
+    def _callback(self, name):
+        def call(*a):
+            self.calls.append(name)
+            self.args[name] = a
+            self.structs[name] = [kind.from_buffer_copy(ctypes.string_at(a[i], ctypes.sizeof(kind))) if a[i] else None
+                                  for i, kind in self.STRUCTS[name]]
+            return self.status
+        kinds = [t if t in (ctypes.c_int, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t) else ctypes.c_void_p
+                 for t in getattr(ops.lib(), name).argtypes]
+        return ctypes.CFUNCTYPE(ctypes.c_int, *kinds)(call)
 
 
 @pytest.fixture
-def rec(monkeypatch):
-    r = _Recorder(ops.lib())
-    monkeypatch.setattr(ops, "lib", lambda: r)
-    monkeypatch.setattr(ops, "_device_of", lambda t: -1)  # CPU tensors stand in for device ones
-    monkeypatch.setattr(ops, "_stream_ptr", lambda stream, dev: None)
-    return r
+def rec():
+    """The marshalling module bound to a recorder; CPU tensors stand in for
+    device ones."""
+    r, m = _Recorder(), ops._attention()
+
+    def bind(fns, any_device):
+        m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (*fns, ops.lib().nvfp4_fp8_kv_attention_workspace_bytes)), any_device)
+    bind(r.keep, True)
+    yield r
+    bind([getattr(ops.lib(), n) for n in r.NAMES], False)
 
 
 bf16, i32 = torch.bfloat16, torch.int32
@@ -217,24 +239,20 @@ BAD = {
     "attend: out overlaps itself": lambda: ops.fp8_kv_attention(Q, *_cache(), out=torch.zeros(3, 1, 256, dtype=bf16).expand(3, 24, 256)),
     "attend: small workspace": lambda: ops.fp8_kv_attention(Q, *_cache(), ws=torch.zeros(16, dtype=torch.uint8)),
     "attend: strided workspace": lambda: ops.fp8_kv_attention(Q, *_cache(), ws=torch.zeros(1 << 27, dtype=torch.uint8)[::2]),
+    "norm: not a tensor": lambda: ops.qk_norm_rope(Q, None, [0, 1, 2], F),
+    "norm: eps not a number": lambda: ops.qk_norm_rope(Q, None, POS, F, eps="x"),
+    "norm: not a stream": lambda: ops.qk_norm_rope(Q, None, POS, F, stream=7),
+    "norm: a stream of nonsense": lambda: ops.qk_norm_rope(Q, None, POS, F, stream=types.SimpleNamespace(cuda_stream="x")),
+    "norm: too many frequencies": lambda: ops.qk_norm_rope(Q, None, POS, torch.ones(1025)),
+    "attend: pages not a tensor": lambda: ops.fp8_kv_attention(Q, None, *_cache()[1:], ws=torch.zeros(16)),
+    "attend: no kv heads": lambda: ops.fp8_kv_attention(Q, *_cache(k=P[:, :, :0], v=P[:, :, :0])),
     "attend: amax too small": lambda: ops.fp8_kv_attention(Q, *_cache(), out_amax=torch.zeros(2, dtype=torch.uint8)),
 }
 
 
-def test_packed_structs_have_the_layout_of_the_header(rec):
+def test_structs_hold_what_the_tensors_say(rec):
     """The host structs that a call packs, read back field by field."""
-    seen = {}
-
-    def keep(name, *specs):
-        def call(*a):
-            seen[name] = [kind.from_buffer_copy(ctypes.string_at(a[i], ctypes.sizeof(kind))) for i, kind in specs]
-            return 0
-        return call
-    for name, specs in (("nvfp4_qk_norm_rope", ((0, ops.Heads), (1, ops.Heads), (2, ops.Heads), (3, ops.Heads), (7, ops.NormRope))),
-                        ("nvfp4_fp8_kv_append", ((0, ops.Heads), (1, ops.Heads), (3, ops.KvPages), (4, ops.KvBatch), (6, ops.NormRope))),
-                        ("nvfp4_fp8_kv_attention", ((0, ops.Heads), (1, ops.Heads), (2, ops.Heads), (4, ops.KvPages), (5, ops.KvBatch),
-                                                    (6, ops.AttentionOpts)))):
-        rec.__dict__[name] = keep(name, *specs)
+    seen = rec.structs
 
     def same(x, **want):
         for k, v in want.items():
@@ -268,6 +286,31 @@ def test_packed_structs_have_the_layout_of_the_header(rec):
     same(pg, **pages)
     same(bt, **batch)
     same(op, softmax_scale=0.5, flags=0)
+
+
+def test_other_arguments_arrive(rec):
+    amax, ws, stream = torch.zeros(1, dtype=i32), torch.zeros(1 << 27, dtype=torch.uint8), types.SimpleNamespace(cuda_stream=0x1230)
+    ops.qk_norm_rope(Q, None, POS, F, stream=stream)
+    a = rec.args["nvfp4_qk_norm_rope"]
+    assert a[1] is None and a[3] is None and a[4:7] == (3, 256, POS.data_ptr()) and a[8] == 0x1230
+    ops.fp8_kv_append(K, K, *_cache(), positions=POS, stream=stream)
+    a = rec.args["nvfp4_fp8_kv_append"]
+    assert a[2] == 3 and a[5] == POS.data_ptr() and a[7] == 0x1230
+    ops.fp8_kv_append(K, K, *_cache())
+    assert rec.args["nvfp4_fp8_kv_append"][5] is None
+    ops.fp8_kv_attention(Q, *_cache(), out_amax=amax, ws=ws, stream=stream)
+    a = rec.args["nvfp4_fp8_kv_attention"]
+    assert a[1] is None and a[3] == 3 and a[7:] == (amax.data_ptr(), ws.data_ptr(), 1 << 27, 0x1230)
+    assert rec.structs["nvfp4_fp8_kv_attention"][5].softmax_scale == 0.0625
+
+
+def test_a_status_is_raised(rec):
+    rec.status = 3
+    for call in (lambda: ops.qk_norm_rope(Q, None, POS, F), lambda: ops.fp8_kv_append(K, K, *_cache()),
+                 lambda: ops.fp8_kv_attention(Q, *_cache())):
+        with pytest.raises(ops.Nvfp4Error) as e:
+            call()
+        assert e.value.code == 3
 
 
 @pytest.mark.parametrize("case", sorted(GOOD))
