@@ -229,8 +229,8 @@ attn::Parts parts_at(uint8_t *base, int64_t rows)
 }
 
 // Which kernels a call launches, and the cost of their items in keys.
-constexpr int32_t kMixedSeqs = 8, kPadRows = 8;
-constexpr int32_t kTileItemCost = 512, kDecodeItemCost = 128;
+constexpr int32_t kMixedItems = 370, kPadRows = 8;
+constexpr int32_t kTileItemCost256 = 1152, kTileItemCost128 = 512, kDecodeItemCost = 128;
 
 // Heads that one warp of the row kernels takes: one while the rows do not
 // fill the GPU, then as many as make a few warps for every place, up to
@@ -419,7 +419,7 @@ extern "C" int nvfp4_fp8_kv_attention(const nvfp4_heads *q, const nvfp4_heads *g
     // one padded by a few rows, may hold both kinds; else it is prompts alone.
     const int64_t group = q->heads / cache->kv_heads;
     const bool single = group <= attn::DECODE_ROWS &&
-                        (batch->num_seqs >= kMixedSeqs || tokens <= int64_t(batch->num_seqs) + kPadRows);
+                        (int64_t(batch->num_seqs) * cache->kv_heads >= kMixedItems || tokens <= int64_t(batch->num_seqs) + kPadRows);
     const bool tiled = !single || tokens > batch->num_seqs;
     attn::AttnParams p;
     p.q = rows_of(q);
@@ -454,7 +454,7 @@ extern "C" int nvfp4_fp8_kv_attention(const nvfp4_heads *q, const nvfp4_heads *g
         p.tile_tokens = k == 0 ? attn::ROW_TILE / p.group : 1;
         p.batch.fresh_min = k == 0 && single ? 2 : 1;
         p.batch.fresh_max = k == 0 || !tiled ? INT32_MAX : 1;
-        p.batch.item_cost = k == 0 ? kTileItemCost : kDecodeItemCost;
+        p.batch.item_cost = k != 0 ? kDecodeItemCost : cache->head_dim == 256 ? kTileItemCost256 : kTileItemCost128;
         if (k == 0)
             launch(cache->head_dim == 256 ? attn::paged_attention_kernel<256> : attn::paged_attention_kernel<128>,
                    dim3(attn::CTAS), dim3(attn::ATTN_THREADS),

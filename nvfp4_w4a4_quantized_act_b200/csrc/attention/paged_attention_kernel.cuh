@@ -78,7 +78,7 @@ constexpr int ROW_WARP0 = 4;        // warps 4..7: one thread per row
 constexpr int SOFT_WARP0 = 8;       // warps 8..15: softmax
 constexpr int SOFT_THREADS = 256;
 constexpr int STAGE_LD = 36;        // floats of a row of the results' staging: 32 columns, spread over the banks
-constexpr uint64_t ATTN_WAIT_NS = 2000000000ull;
+constexpr uint64_t ATTN_WAIT_NS = 2000000000ull, ATTN_DRAIN_NS = 10000000ull;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr float P_SHIFT = 8.0f;       // probabilities are 2^(t - r + P_SHIFT)
 constexpr float REF_UP = 0.75f;       // 2^(P_SHIFT + REF_UP) < 448
@@ -235,20 +235,27 @@ __device__ __forceinline__ void split_query(const uint4 &v, uint2 &hi, uint2 &lo
     split8(v, scale, hi, lo);
 }
 
+// Four columns of the gate's row; of no effect without a gate.
+__device__ __forceinline__ uint2 load_gate4(const AttnParams &p, int32_t token, int32_t head, int col)
+{
+    uint2 g = make_uint2(0, 0);
+    if (p.gate.data != nullptr)
+        g = *reinterpret_cast<const uint2 *>(p.gate.data + token * p.gate.token_stride + head * p.gate.head_stride + col);
+    return g;
+}
+
 // Four columns of an output row: sums times inv (zeros where the row saw no
 // key), the gate, bf16.  Returns the running max|out| (two bf16 magnitudes).
-__device__ __forceinline__ uint32_t write_row4(const AttnParams &p, const float (&o)[4], float inv, bool empty, int32_t token,
-                                               int32_t head, int col, uint32_t amax)
+__device__ __forceinline__ uint32_t write_row4(const AttnParams &p, const float (&o)[4], float inv, bool empty, const uint2 &gate,
+                                               int32_t token, int32_t head, int col, uint32_t amax)
 {
     float y[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
         y[e] = empty ? 0.0f : o[e] * inv;
     if (p.gate.data != nullptr) {
-        const uint2 gw = *reinterpret_cast<const uint2 *>(p.gate.data + token * p.gate.token_stride +
-                                                          head * p.gate.head_stride + col);
-        const float gx[4] = {__uint_as_float(gw.x << 16), __uint_as_float(gw.x & 0xFFFF0000u),
-                             __uint_as_float(gw.y << 16), __uint_as_float(gw.y & 0xFFFF0000u)};
+        const float gx[4] = {__uint_as_float(gate.x << 16), __uint_as_float(gate.x & 0xFFFF0000u),
+                             __uint_as_float(gate.y << 16), __uint_as_float(gate.y & 0xFFFF0000u)};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             y[e] = __fdividef(y[e], 1.0f + __expf(-gx[e]));
@@ -257,6 +264,20 @@ __device__ __forceinline__ uint32_t write_row4(const AttnParams &p, const float 
     const uint2 w = make_uint2(*reinterpret_cast<const uint32_t *>(&b0), *reinterpret_cast<const uint32_t *>(&b1));
     *reinterpret_cast<uint2 *>(const_cast<uint16_t *>(p.out.data) + token * p.out.token_stride + head * p.out.head_stride + col) = w;
     return __vmaxu2(__vmaxu2(amax, w.x & 0x7FFF7FFFu), w.y & 0x7FFF7FFFu);
+}
+
+// Eight results times sigmoid(gate) = 1 / (1 + 2^(-gate log2 e)).
+__device__ __forceinline__ void gate8(float (&y)[8], const uint4 &g)
+{
+    const uint32_t w[4] = {g.x, g.y, g.z, g.w};
+    const uint64_t minus_log2e = pack2(-1.4426950408889634f, -1.4426950408889634f), one = pack2(1.0f, 1.0f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint64_t t = mul2(pack2u(w[k] << 16, w[k] & 0xFFFF0000u), minus_log2e);
+        float a, b;
+        unpack2(add2(exp2_fast2(t), one), a, b);
+        unpack2(mul2(pack2(y[2 * k], y[2 * k + 1]), pack2(rcp_fast(a), rcp_fast(b))), y[2 * k], y[2 * k + 1]);
+    }
 }
 
 // A warp's max|out| into the caller's word.
@@ -367,34 +388,42 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
             none.continues = none.owns = none.last = none.token0 = none.rows = none.group0 = none.past0 = none.pad = 0;
             p.parts.info[cta] = none;
         }
-    } else if (warp == 0) {
+    } else if (warp == 0 || warp == 3) {
         // ------------------------------------------------------ loads
+        // Warp 0 fetches the K blocks, warp 3 the V blocks, into the ring in the order K0 K1 V0 K2 V1 .. K(n-1) V(n-2)
+        // V(n-1).  A lane holds the page of one box, 32 boxes at a time and the next 32 on their way: read block by
+        // block, the page table's latency came between any two fetches.
+        const bool is_k = warp == 0;
         const int shift = p.batch.page_shift, page = 1 << shift;
         const int rows = min(page, KEY_BLOCK);        // rows of a box
-        const int boxes = KEY_BLOCK / rows;
-        uint32_t fills = 0;
+        const int row_shift = min(shift, 7), boxes_shift = 7 - row_shift, boxes = 1 << boxes_shift;
+        const CUtensorMap *map = is_k ? &tmK : &tmV;
+        const int row_at = is_k ? p.k_row_at : p.v_row_at, head_at = is_k ? p.k_head_at : p.v_head_at;
+        uint32_t base = 0;  // ring stages of the items before
         bool fail = false, out_of_pool = false;
+        uint32_t filled = 0, phases = 0;  // stages that this warp has filled, and the last time's phases
         for (int i = 0;; ++i) {
             const Item it = take_item(i, fail);
             if (!__all_sync(0xFFFFFFFFu, !fail) || it.blocks == 0)
                 break;
             const int32_t *table = p.batch.table + it.seq * p.batch.table_stride;
-            const int t1 = it.t0 + it.blocks;
-            // this lane's box of block t has keys, and lies in page:
-            auto wanted = [&](int t) { return t < t1 && lane < boxes && t * KEY_BLOCK + lane * rows < it.keys; };
-            auto page_of = [&](int t) { return wanted(t) ? __ldg(table + ((t * KEY_BLOCK + lane * rows) >> shift)) : 0; };
-            int32_t id = page_of(it.t0), id_next = page_of(it.t0 + 1);  // of blocks t and t + 1
-            int t = it.t0;
-            // K0 K1 V0 K2 V1 .. K(n-1) V(n-2) V(n-1)
+            const int box0 = it.t0 << boxes_shift, box1 = min((it.t0 + it.blocks) << boxes_shift, (it.keys + rows - 1) >> row_shift);
+            auto page_of = [&](int box) { return box < box1 ? __ldg(table + ((box << row_shift) >> shift)) : 0; };
+            int32_t ids = page_of(box0 + lane), next = page_of(box0 + 32 + lane);
 #pragma unroll 1
-            for (int step = 0; step < 2 * it.blocks; ++step) {
-                const bool is_k = step == 0 || ((step & 1) && step < 2 * it.blocks - 1);
-                const int block = is_k && step ? t + 1 : t;
-                const int32_t at = is_k && step ? id_next : id;
-                const uint32_t stage = fills % A::STAGES, phase = (fills / A::STAGES) & 1u;
-                const uint32_t bar = smem_u32(&sm->full[stage]);
-                const bool mine = wanted(block);
+            for (int j = 0; j < it.blocks; ++j) {
+                const int at = j << boxes_shift;  // first box of the block, from box0
+                if (j > 0 && (at & 31) == 0) {
+                    ids = next;
+                    next = page_of(box0 + at + 32 + lane);
+                }
+                const int32_t id = __shfl_sync(0xFFFFFFFFu, ids, (at + lane) & 31);
+                const int box = box0 + at + lane;
+                const bool mine = lane < boxes && box < box1;
                 const int count = __popc(__ballot_sync(0xFFFFFFFFu, mine));
+                const uint32_t fill = base + (is_k ? max(2 * j - 1, 0) : ring_v(j, it.blocks));
+                const uint32_t stage = fill % A::STAGES, phase = (fill / A::STAGES) & 1u;
+                const uint32_t bar = smem_u32(&sm->full[stage]);
                 if (lane == 0) {
                     if (mbar_wait(smem_u32(&sm->empty[stage]), phase ^ 1u, ATTN_WAIT_NS))
                         mbar_arrive_expect_tx(bar, static_cast<uint32_t>(count * rows * D));
@@ -405,33 +434,29 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
                 if (fail)
                     break;
                 if (mine) {
-                    const int row = (block * KEY_BLOCK + lane * rows) & (page - 1);
+                    const int row = (box << row_shift) & (page - 1);
                     const uint32_t dst = ring + stage * A::STAGE_BYTES + lane * rows * 128;
-                    const CUtensorMap *map = is_k ? &tmK : &tmV;
-                    const int row_at = is_k ? p.k_row_at : p.v_row_at, head_at = is_k ? p.k_head_at : p.v_head_at;
-                    const int32_t c1 = row_at == 1 ? row : head_at == 1 ? it.head : at;
-                    const int32_t c2 = row_at == 2 ? row : head_at == 2 ? it.head : at;
-                    const int32_t c3 = row_at == 3 ? row : head_at == 3 ? it.head : at;
+                    const int32_t c1 = row_at == 1 ? row : head_at == 1 ? it.head : id;
+                    const int32_t c2 = row_at == 2 ? row : head_at == 2 ? it.head : id;
+                    const int32_t c3 = row_at == 3 ? row : head_at == 3 ? it.head : id;
 #pragma unroll
                     for (int s = 0; s < A::SUBS; ++s)
                         tma_load_4d(dst + s * A::SUB_BYTES, map, s * 128, c1, c2, c3, bar);
+                    out_of_pool |= id < 0 || id >= p.batch.num_pages;
                 }
-                ++fills;
-                if (!is_k) {
-                    out_of_pool |= mine && (id < 0 || id >= p.batch.num_pages);
-                    ++t;
-                    id = id_next;
-                    id_next = page_of(t + 1);
-                }
+                filled |= 1u << stage;
+                phases = (phases & ~(1u << stage)) | phase << stage;
             }
+            base += 2 * it.blocks;
         }
         if (out_of_pool)
             atomicOr(p.status, kStatusBadIndex);
         if (fail && lane == 0) {
             attn_timeout(sm, p.status);
             // copies in flight land before the shared memory goes away
-            for (uint32_t f = fills > A::STAGES ? fills - A::STAGES : 0; f < fills; ++f)
-                mbar_wait(smem_u32(&sm->full[f % A::STAGES]), (f / A::STAGES) & 1u, ATTN_WAIT_NS);
+            for (int f = 0; f < A::STAGES; ++f)
+                if (filled >> f & 1u)
+                    mbar_wait(smem_u32(&sm->full[f]), phases >> f & 1u, ATTN_DRAIN_NS);
         }
     } else if (warp == 1) {
         // ------------------------------------------------------ MMAs
@@ -678,6 +703,27 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
             }
             uses += 2 * it.blocks;
             // ------------------------------------------------ results
+            // 32 columns at a time, a lane 8 columns of every 8th row.  Addresses, and the gate's first columns on their
+            // way, while the last values are being added up; then the next columns' while these are worked on.
+            const bool whole = it.part == 0, gated = whole && p.gate.data != nullptr;
+            const int rows_here = it.rows - quarter * 32, sub = lane >> 2, c8 = (lane & 3) * 8;
+            const uint16_t *gate_at[4];
+            uint16_t *out_at[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t r = quarter * 32 + e * 8 + sub, tk = r * p.group_inv >> 16;
+                const int32_t t = it.token0 + tk, h = it.head * p.group + (r - tk * p.group);
+                gate_at[e] = p.gate.data + t * p.gate.token_stride + h * p.gate.head_stride + c8;
+                out_at[e] = const_cast<uint16_t *>(p.out.data) + t * p.out.token_stride + h * p.out.head_stride + c8;
+            }
+            uint4 gv[4] = {};
+            auto load_gate = [&](int col) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (gated && col < D && e * 8 + sub < rows_here)
+                        gv[e] = *reinterpret_cast<const uint4 *>(gate_at[e] + col);
+            };
+            load_gate(0);
             wait(sm->stats_ready, i);
             if (it.blocks > 0)
                 wait_values(block - 1);
@@ -686,37 +732,22 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
                 break;
             tc_fence_after();
             const float total = sm->sum[ip][0][row] + sm->sum[ip][1][row];
-            const bool whole = it.part == 0, has_nan = sm->nan_any[ip] != 0;
+            const bool has_nan = sm->nan_any[ip] != 0;
             const float factor = whole ? vs / total : 1.0f;
-            if (quarter * 32 < it.rows) {
-                // The accumulator has a row per lane; memory wants a row's columns together: 32 columns at a
-                // time pass through shared memory, and 4 lanes take a row's 8 columns each.
-                const int sub = lane >> 2, c8 = (lane & 3) * 8;
-                const int64_t prow0 = (static_cast<int64_t>(cta) * 2 + (it.part == 2 ? 1 : 0)) * p.parts.rows;
-                int64_t out_at[4], gate_at[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t r = quarter * 32 + e * 8 + sub, tk = r * p.group_inv >> 16;
-                    const int32_t t = it.token0 + tk, h = it.head * p.group + (r - tk * p.group);
-                    out_at[e] = whole ? t * p.out.token_stride + h * p.out.head_stride + c8 : (prow0 + r) * D + c8;
-                    gate_at[e] = t * p.gate.token_stride + h * p.gate.head_stride + c8;
-                }
-#pragma unroll 1
-                for (int col = 0; col < D; col += 32) {
+            const uint64_t ff = pack2(factor, factor);
+            if (rows_here > 0) {
+                // The accumulator has a row per lane; memory wants a row's columns together: 32 columns at a time
+                // pass through shared memory, and a lane takes 16 bytes of every 8th row (results) or 4th (parts).
+                auto stage = [&](int col) {
                     uint32_t o[32];
-                    uint4 gv[4];
-                    if (whole && p.gate.data != nullptr) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (quarter * 32 + e * 8 + sub < it.rows)
-                                gv[e] = *reinterpret_cast<const uint4 *>(p.gate.data + gate_at[e] + col);
-                    }
                     tc_ld_32x32b_x32(tmem + A::O_COL + col + lanes, o);
                     tc_wait_ld();
+                    __syncwarp();
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
-                        const float4 y = make_float4(__uint_as_float(o[e]) * factor, __uint_as_float(o[e + 1]) * factor,
-                                                     __uint_as_float(o[e + 2]) * factor, __uint_as_float(o[e + 3]) * factor);
+                        float4 y;
+                        unpack2(mul2(pack2u(o[e], o[e + 1]), ff), y.x, y.y);
+                        unpack2(mul2(pack2u(o[e + 2], o[e + 3]), ff), y.z, y.w);
                         *reinterpret_cast<float4 *>(stage_rows + lane * STAGE_LD + e) = y;
                     }
                     if (live && (seen == 0 || has_nan)) {  // no key in sight, or perhaps a NaN
@@ -729,36 +760,55 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
                         }
                     }
                     __syncwarp();
+                };
+                if (whole) {
+#pragma unroll 1
+                    for (int col = 0; col < D; col += 32) {
+                        stage(col);
+                        // all four rows at once: a branch between them would leave their latencies in a row
+                        float y[4][8];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float *src = stage_rows + (e * 8 + sub) * STAGE_LD + c8;
-                        const float4 a = *reinterpret_cast<const float4 *>(src), b = *reinterpret_cast<const float4 *>(src + 4);
-                        if (quarter * 32 + e * 8 + sub >= it.rows)
-                            continue;
-                        if (whole) {
-                            float y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-                            if (p.gate.data != nullptr) {
-                                float gx[8];
-                                unpack8(gv[e], gx);
+                        for (int e = 0; e < 4; ++e)
 #pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    y[k] = __fdividef(y[k], 1.0f + __expf(-gx[k]));
+                            for (int k = 0; k < 8; k += 4)
+                                *reinterpret_cast<float4 *>(&y[e][k]) =
+                                    *reinterpret_cast<const float4 *>(stage_rows + (e * 8 + sub) * STAGE_LD + c8 + k);
+                        if (gated) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                gate8(y[e], gv[e]);
+                        }
+                        load_gate(col + 32);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint4 w = pack8(y[e]);
+                            if (e * 8 + sub < rows_here) {
+                                *reinterpret_cast<uint4 *>(out_at[e] + col) = w;
+                                if (p.out_amax == nullptr)
+                                    continue;
+                                amax = __vmaxu2(__vmaxu2(amax, w.x & 0x7FFF7FFFu), w.y & 0x7FFF7FFFu);
+                                amax = __vmaxu2(__vmaxu2(amax, w.z & 0x7FFF7FFFu), w.w & 0x7FFF7FFFu);
                             }
-                            const uint4 w = pack8(y);
-                            *reinterpret_cast<uint4 *>(const_cast<uint16_t *>(p.out.data) + out_at[e] + col) = w;
-                            amax = __vmaxu2(__vmaxu2(amax, w.x & 0x7FFF7FFFu), w.y & 0x7FFF7FFFu);
-                            amax = __vmaxu2(__vmaxu2(amax, w.z & 0x7FFF7FFFu), w.w & 0x7FFF7FFFu);
-                        } else {
-                            float4 *op = reinterpret_cast<float4 *>(p.parts.o + out_at[e] + col);
-                            op[0] = a;
-                            op[1] = b;
                         }
                     }
-                    __syncwarp();
-                }
-                if (!whole && live) {
-                    p.parts.ml[(prow0 + row) * 2] = sm->ref[ip][row];
-                    p.parts.ml[(prow0 + row) * 2 + 1] = total;
+                } else {
+                    const int64_t prow0 = (static_cast<int64_t>(cta) * 2 + (it.part == 2 ? 1 : 0)) * p.parts.rows + quarter * 32;
+                    float *to = p.parts.o + (prow0 + (lane >> 3)) * D + (lane & 7) * 4;
+                    const float *from = stage_rows + (lane >> 3) * STAGE_LD + (lane & 7) * 4;
+#pragma unroll 1
+                    for (int col = 0; col < D; col += 32) {
+                        stage(col);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float4 a = *reinterpret_cast<const float4 *>(from + e * 4 * STAGE_LD);
+                            if (e * 4 + (lane >> 3) < rows_here)
+                                *reinterpret_cast<float4 *>(to + e * 4 * D + col) = a;
+                        }
+                    }
+                    if (live) {
+                        p.parts.ml[(prow0 + lane) * 2] = sm->ref[ip][row];
+                        p.parts.ml[(prow0 + lane) * 2 + 1] = total;
+                    }
                 }
             }
             tc_fence_before();
@@ -792,9 +842,9 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
             if (!fail && it.blocks == 0)
                 break;
             // Queries to shared memory as two E4M3 terms (the score MMAs of the item before have completed): each
-            // warp takes every 8th row, or pair of rows, BATCH loads in flight
+            // warp takes every 8th row, or pair of rows, eight rows at a time and the other eight on their way
             {
-                constexpr int LANES = D / 8, GROUP = 32 / LANES, BATCH = 4;
+                constexpr int LANES = D / 8, GROUP = 32 / LANES, BATCH = 8 / GROUP;
                 const int col = (lane % LANES) * 8;
                 const uint16_t *src = p.q.data + it.token0 * p.q.token_stride + it.head * p.group * p.q.head_stride + col;
                 auto load = [&](int r0, uint4 (&v)[BATCH]) {
@@ -814,17 +864,15 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
                     load(r0 + 8 * GROUP * BATCH, next);
 #pragma unroll
                     for (int e = 0; e < BATCH; ++e) {
-                        const int r = r0 + 8 * GROUP * e + lane / LANES;
+                        const int r = r0 + 8 * GROUP * e + lane / LANES;  // below 128
                         uint2 hi, lo;
                         float unscale;
                         split_query<D>(v[e], hi, lo, unscale);
-                        if (r < ROW_TILE) {
-                            uint8_t *at = smem + (col >> 7) * A::SUB_BYTES + r * 128 + ((col & 127) ^ ((r & 7) << 4));
-                            *reinterpret_cast<uint2 *>(at) = hi;
-                            *reinterpret_cast<uint2 *>(at + A::SUBS * A::SUB_BYTES) = lo;
-                            if ((lane % LANES) == 0)
-                                sm->row_scale[r] = unscale;
-                        }
+                        uint8_t *at = smem + (col >> 7) * A::SUB_BYTES + r * 128 + ((col & 127) ^ ((r & 7) << 4));
+                        *reinterpret_cast<uint2 *>(at) = hi;
+                        *reinterpret_cast<uint2 *>(at + A::SUBS * A::SUB_BYTES) = lo;
+                        if ((lane % LANES) == 0)
+                            sm->row_scale[r] = unscale;
                         v[e] = next[e];
                     }
                 }
@@ -839,7 +887,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
             const bool live = row < it.rows, warp_live = quarter * 32 < it.rows;
             // keys in sight of this half row, from the current block's first; rows that no token fills need no mask
             int vis = live ? max(it.past0 + static_cast<int>(row * p.group_inv >> 16) + 1, 0) - it.t0 * KEY_BLOCK - half * 64 : INT_MAX;
-            float f = 0.0f, ref = 0.0f, top = -INFINITY;
+            float f = 0.0f, ref = -INFINITY, top = -INFINITY;
             if (live) {
                 f = sm->row_scale[row] * c;
                 f = f < 1.17549435e-38f ? 1.17549435e-38f : f;  // keeps (-inf) * f; NaN stays
@@ -880,19 +928,16 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
                 if (warp_live) {
                     const float2 other = sm->red[buf][half ^ 1][row];
                     const float tm = fmaxf(mine, other.x) * f;
-                    if (tm > -INFINITY) {
-                        const bool begun = top > -INFINITY;
-                        top = fmaxf(top, tm);
-                        if (!begun) {
-                            ref = tm + SLACK_UP;
-                        } else {
-                            const bool up = tm > ref + REF_UP;
-                            if (up || (tm < ref - REF_DOWN && so_far + other.y < BLOCK_SUM * static_cast<float>(j))) {
-                                const float to = fmaxf(tm + (up ? SLACK_UP : SLACK_DOWN), top - REF_SPAN);
-                                turn = exp2_fast(ref - to);
-                                sum2 = mul2(sum2, pack2(turn, turn));
-                                ref = to;
-                            }
+                    // ref is -inf until the row has seen a key; one branch for the warp, few blocks take it
+                    const bool up = tm > ref + REF_UP;
+                    const bool down = tm < ref - REF_DOWN && so_far + other.y < BLOCK_SUM * static_cast<float>(j) && tm > -INFINITY;
+                    top = fmaxf(top, tm);
+                    if (__any_sync(0xFFFFFFFFu, up || down)) {
+                        if (up || down) {
+                            const float to = fmaxf(tm + (up ? SLACK_UP : SLACK_DOWN), top - REF_SPAN);
+                            turn = ref > -INFINITY ? exp2_fast(ref - to) : 1.0f;
+                            ref = to;
+                            sum2 = mul2(sum2, pack2(turn, turn));
                         }
                     }
                 }
@@ -902,7 +947,8 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
                     if (lane == 0)
                         mbar_arrive(smem_u32(&sm->turn_ready[buf]));
                 }
-                const uint64_t bb = pack2(P_SHIFT - ref, P_SHIFT - ref);
+                const float shift = P_SHIFT - (ref > -INFINITY ? ref : 0.0f);
+                const uint64_t bb = pack2(shift, shift);
                 uint64_t sum_b = 0;
                 // Scores are read from TMEM a second time, 32 at a time, instead of being held: the loop's code is
                 // half as long, and the warps' loops together have to fit the instruction cache.
@@ -918,8 +964,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
                                 const uint64_t t = fma2(pack2u(v[4 * k + 2 * e], v[4 * k + 2 * e + 1]), ff, bb);
-                                // three of four pairs on the special-function unit, one on the FMA pipe
-                                x[e] = (2 * k + e) % 4 == 3 ? exp2_poly2(t) : exp2_fast2(t);
+                                x[e] = exp2_fast2(t);
                                 y[e] = x[e] & 0xFFF00000FFF00000ull;
                                 z[e] = fma2(y[e], neg, x[e]);
                             }
@@ -967,10 +1012,17 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
 // per row; the parts are added in the order of their keys.  A second set of
 // parts (of the kernel for single tokens beside this one's) follows the first
 // in the grid.
-constexpr int JOIN_ROWS = 8;
+//
+// The bytes are few (D floats a part and row); what counts is how many loads
+// wait for one another and how many rows are in flight.  Once a row's item is
+// known, its gate, its parts' states and, where JOIN_AHEAD CTAs or fewer share
+// it, their sums are asked for at once, and 64 registers leave room for 32 warps on an SM: with
+// 107 and the loads one after the other the join of 148 x 126 rows of 256
+// took 33 us.
+constexpr int JOIN_ROWS = 8, JOIN_AHEAD = 4;
 
 template <int D>
-__global__ void __launch_bounds__(JOIN_ROWS * 32) paged_attention_join_kernel(const AttnParams p, const Parts second)
+__global__ void __launch_bounds__(JOIN_ROWS * 32, 4) paged_attention_join_kernel(const AttnParams p, const Parts second)
 {
     grid_dep_wait();
     grid_dep_launch_dependents();
@@ -981,56 +1033,84 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32) paged_attention_join_kernel(co
     const float ks = __ldg(p.k_scale), vs = __ldg(p.v_scale);
     if (!info.owns || row >= info.rows || !valid_scale(ks) || !valid_scale(vs))
         return;
-    // A lane for every CTA of a span of 32: which hold a part, and their references and sums, all loads at once
+    constexpr int PER = D / 128;
+    const int tk = row / p.group, h = info.group0 + row - tk * p.group;
     auto slot_of = [&](int c) { return (static_cast<int64_t>(c) * 2 + (c == cta ? 1 : 0)) * parts.rows + row; };
-    auto state = [&](int c, float2 &ml) {
-        const bool in = c <= info.last;
-        const bool has = in && (c == cta || parts.info[c].continues != 0);
-        ml = make_float2(-INFINITY, 0.0f);
-        if (in)
-            ml = *reinterpret_cast<const float2 *>(parts.ml + slot_of(c) * 2);
-        return has;
+    int pick[JOIN_AHEAD];  // CTAs whose parts are in x, from the span's first; -1: none
+    float4 x[JOIN_AHEAD][PER];
+    auto load = [&](int c0) {
+#pragma unroll
+        for (int e = 0; e < JOIN_AHEAD; ++e) {
+            const float *src = parts.o + slot_of(c0 + max(pick[e], 0)) * D + lane * 4;
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (pick[e] >= 0)
+                    x[e][i] = *reinterpret_cast<const float4 *>(src + i * 128);
+        }
     };
-    float top = -INFINITY;
-    for (int c = cta + lane; c - lane <= info.last; c += 32) {
-        float2 ml;
-        if (state(c, ml))
-            top = fmaxf(top, ml.x);
+    // A lane for every CTA of a span of 32: which hold a part, and their references and sums
+    auto state = [&](int c, float2 &ml) {
+        ml = make_float2(-INFINITY, 0.0f);
+        if (c > info.last)
+            return false;
+        ml = *reinterpret_cast<const float2 *>(parts.ml + slot_of(c) * 2);
+        return c == cta || parts.info[c].continues != 0;
+    };
+    uint2 gate[PER];
+    float2 ml;
+    bool has = state(cta + lane, ml);
+    // Few CTAs: all their sums are read before it is known which of them hold a part
+    const bool near = info.last - cta < JOIN_AHEAD;
+    if (near) {
+#pragma unroll
+        for (int e = 0; e < JOIN_AHEAD; ++e)
+            pick[e] = cta + e <= info.last ? e : -1;
+        load(cta);
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        gate[i] = load_gate4(p, info.token0 + tk, h, i * 128 + lane * 4);
+    float top = has ? ml.x : -INFINITY;
+    for (int c = cta + 32 + lane; c - lane <= info.last; c += 32) {
+        float2 more;
+        if (state(c, more))
+            top = fmaxf(top, more.x);
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
-    constexpr int PER = D / 32;
-    float o[PER], sum = 0.0f;
+    float o[4 * PER], sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
+    for (int i = 0; i < 4 * PER; ++i)
         o[i] = 0.0f;
+#pragma unroll 1
     for (int c0 = cta; c0 <= info.last; c0 += 32) {
-        float2 ml;
-        uint32_t todo = __ballot_sync(0xFFFFFFFFu, state(c0 + lane, ml));
+        if (c0 > cta)
+            has = state(c0 + lane, ml);
+        uint32_t todo = __ballot_sync(0xFFFFFFFFu, has);
+        const uint32_t there = todo;
         // no key in sight in any part: weight 1 keeps the zero or NaN sums
         const float mine = top > -INFINITY ? exp2_fast(ml.x - top) : 1.0f;
+#pragma unroll 1
         while (todo) {
-            // eight parts' sums at a time
-            int k[8];
-            float4 x[8][PER / 4];
+            if (near) {
+                todo = 0;
+            } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                k[e] = todo ? __ffs(todo) - 1 : -1;
-                todo &= todo - 1;
-                const float *src = parts.o + slot_of(c0 + max(k[e], 0)) * D + lane * 4;
-#pragma unroll
-                for (int i = 0; i < PER / 4; ++i)
-                    x[e][i] = k[e] >= 0 ? *reinterpret_cast<const float4 *>(src + i * 128) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int e = 0; e < JOIN_AHEAD; ++e) {
+                    pick[e] = todo ? __ffs(todo) - 1 : -1;
+                    todo &= todo - 1;
+                }
+                load(c0);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (k[e] < 0)
-                    break;
-                const float w = __shfl_sync(0xFFFFFFFFu, mine, k[e]);
-                sum = fmaf(w, __shfl_sync(0xFFFFFFFFu, ml.y, k[e]), sum);
+            for (int e = 0; e < JOIN_AHEAD; ++e) {
+                if (pick[e] < 0 || !(there >> pick[e] & 1u))
+                    continue;
+                const float w = __shfl_sync(0xFFFFFFFFu, mine, pick[e]);
+                sum = fmaf(w, __shfl_sync(0xFFFFFFFFu, ml.y, pick[e]), sum);
 #pragma unroll
-                for (int i = 0; i < PER / 4; ++i) {
+                for (int i = 0; i < PER; ++i) {
                     o[4 * i] = fmaf(w, x[e][i].x, o[4 * i]);
                     o[4 * i + 1] = fmaf(w, x[e][i].y, o[4 * i + 1]);
                     o[4 * i + 2] = fmaf(w, x[e][i].z, o[4 * i + 2]);
@@ -1039,13 +1119,12 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32) paged_attention_join_kernel(co
             }
         }
     }
-    const int tk = row / p.group, h = info.group0 + row - tk * p.group;
     const float inv = vs / sum;
     uint32_t amax = 0;
 #pragma unroll
-    for (int i = 0; i < PER / 4; ++i) {
+    for (int i = 0; i < PER; ++i) {
         const float y[4] = {o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]};
-        amax = write_row4(p, y, inv, info.past0 + tk < 0, info.token0 + tk, h, i * 128 + lane * 4, amax);
+        amax = write_row4(p, y, inv, info.past0 + tk < 0, gate[i], info.token0 + tk, h, i * 128 + lane * 4, amax);
     }
     store_amax(p, amax, lane);
 }

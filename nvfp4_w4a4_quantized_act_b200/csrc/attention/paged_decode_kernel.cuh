@@ -548,7 +548,8 @@ __global__ void __launch_bounds__(DECODE_THREADS, 1)
                     y[3] = fmaf(a, x.w, y[3]);
                 }
                 if (whole) {
-                    amax = write_row4(p, y, vs / total, it.past0 < 0, it.token0, it.head * p.group + r, col, amax);
+                    const int32_t h = it.head * p.group + r;
+                    amax = write_row4(p, y, vs / total, it.past0 < 0, load_gate4(p, it.token0, h, col), it.token0, h, col, amax);
                 } else {
                     *reinterpret_cast<float4 *>(p.parts.o + (prow0 + r) * D + col) = make_float4(y[0], y[1], y[2], y[3]);
                     if (col == 0) {

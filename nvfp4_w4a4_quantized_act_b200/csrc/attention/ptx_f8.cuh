@@ -212,38 +212,20 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
+// 1 / x to 1 unit in the last place; zero where that is below 2^-126.
+__device__ __forceinline__ float rcp_fast(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // 2^x of a pair on the special-function unit.
 __device__ __forceinline__ uint64_t exp2_fast2(uint64_t t)
 {
     float a, b;
     unpack2(t, a, b);
     return pack2(exp2_fast(a), exp2_fast(b));
-}
-
-__device__ __forceinline__ float max_nan(float a, float b)
-{
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-
-// 2^x of a pair on the FMA and integer pipes, for x < 127: x = n + f with n
-// the nearest integer (adding 1.5 * 2^23 leaves n in the low mantissa bits)
-// and |f| <= 1/2; 2^f by the polynomial of degree 3 that is best in relative
-// error there (below 2^-13.7), and 2^n from its bits.  x is held at -100,
-// where the result stands for zero; a NaN stays one.
-__device__ __forceinline__ uint64_t exp2_poly2(uint64_t t)
-{
-    float a, b, na, nb;
-    unpack2(t, a, b);
-    t = pack2(max_nan(a, -100.0f), max_nan(b, -100.0f));
-    const uint64_t n = add2(t, pack2(12582912.0f, 12582912.0f));
-    const uint64_t f = fma2(add2(n, pack2(-12582912.0f, -12582912.0f)), pack2(-1.0f, -1.0f), t);
-    uint64_t y = fma2(f, pack2(0.0551716462f, 0.0551716462f), pack2(0.24261117f, 0.24261117f));
-    y = fma2(f, y, pack2(0.693260968f, 0.693260968f));
-    y = fma2(f, y, pack2(0.999928057f, 0.999928057f));
-    unpack2(n, na, nb);
-    return mul2(y, pack2u(0x3F800000u + (__float_as_uint(na) << 23), 0x3F800000u + (__float_as_uint(nb) << 23)));
 }
 
 }  // namespace attn
