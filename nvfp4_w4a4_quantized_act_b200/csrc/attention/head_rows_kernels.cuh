@@ -29,6 +29,7 @@ namespace attn {
 
 constexpr int ROW_WARPS = 4;        // warps of a block
 constexpr int MAX_HALF = 128;       // rotated pairs of a head (head_dim <= 256)
+constexpr int UNIT_BYTES = 4096;    // of the rows that a warp takes at most
 
 // cos and sin of pos * f.  The product of a 31-bit position and a 24-bit
 // frequency is held in fp64, multiplied by 1 / 2 pi (in two parts) and reduced
@@ -83,6 +84,17 @@ __device__ __forceinline__ uint4 load_row(const uint16_t *row, const LaneMap &m)
 {
     const uint2 u = *reinterpret_cast<const uint2 *>(row + m.a), v = *reinterpret_cast<const uint2 *>(row + m.b);
     return make_uint4(u.x, u.y, v.x, v.y);
+}
+
+// 16 bytes to shared memory, asynchronously, and the wait for all of them.
+__device__ __forceinline__ void copy16(void *dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_done()
+{
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
 }
 
 // The token's rotations to shared memory (one warp's share), then the lane's 4.
@@ -168,6 +180,7 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) qk_norm_rope_kernel(const Norm
     constexpr int LANES = D / 8;               // lanes of a row
     constexpr int GROUP = 32 / LANES;          // rows of a warp at a time
     __shared__ alignas(16) float2 cs[ROW_WARPS][MAX_HALF];
+    __shared__ alignas(16) uint16_t in_rows[ROW_WARPS][UNIT_BYTES / 2];
     grid_dep_wait();
     grid_dep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -185,21 +198,18 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) qk_norm_rope_kernel(const Norm
     const uint16_t *src = in.data + t * in.token_stride;
     uint16_t *dst = const_cast<uint16_t *>(out.data) + t * out.token_stride;
     int h = u * p.unit_heads + lane / LANES;
-    uint4 v = make_uint4(0, 0, 0, 0), next = v;
-    if (h < h1)
-        v = load_row(src + h * in.head_stride, m);
-    if (h + GROUP < h1)
-        next = load_row(src + (h + GROUP) * in.head_stride, m);
+    const int lane8 = lane % LANES * 8;
+    uint16_t *row = in_rows[warp] + lane / LANES * D;
+    for (int i = 0; h + i < h1; i += GROUP)
+        copy16(row + i * D + lane8, src + (h + i) * in.head_stride + lane8);
     float w[8], c[4], s[4];
     load_weights(p.weight[which], m, p.one, w);
     if (p.half > 0)
         load_rotations(cs[warp], __ldg(p.positions + t), p.inv_freq, p.half, m, lane, c, s);
-    for (int i = u * p.unit_heads; i < h1; i += GROUP, h += GROUP) {  // alike for all lanes
+    copies_done();
+    for (int i = u * p.unit_heads; i < h1; i += GROUP, h += GROUP, row += GROUP * D) {  // alike for all lanes
         float x[8];
-        unpack8(v, x);
-        v = next;
-        if (h + 2 * GROUP < h1)
-            next = load_row(src + (h + 2 * GROUP) * in.head_stride, m);
+        unpack8(load_row(row, m), x);
         norm_rotate<D>(x, p.weight[which] != nullptr, w, p.eps, m.turned, c, s);
         if (h < h1) {
             const uint4 y = pack8(x);
@@ -261,6 +271,7 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) kv_append_kernel(const AppendP
     constexpr int LANES = D / 8;
     constexpr int GROUP = 32 / LANES;
     __shared__ alignas(16) float2 cs[ROW_WARPS][MAX_HALF];
+    __shared__ alignas(16) uint16_t in_rows[ROW_WARPS][UNIT_BYTES / 2];  // keys, and values in the other half
     grid_dep_wait();
     grid_dep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -277,14 +288,14 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) kv_append_kernel(const AppendP
     const int u = static_cast<int>(unit - static_cast<int64_t>(t) * p.units);
     const int h1 = min((u + 1) * p.unit_heads, p.in[0].heads);
     const LaneMap m(lane % LANES, p.half);
-    const LaneMap plain(lane % LANES, 0);
     const uint16_t *k_src = p.in[0].data + t * p.in[0].token_stride, *v_src = p.in[1].data + t * p.in[1].token_stride;
     int h = u * p.unit_heads + lane / LANES;
-    // the first rows are on their way while the token's place is looked up
-    uint4 kv = make_uint4(0, 0, 0, 0), vv = kv;
-    if (h < h1) {
-        kv = load_row(k_src + h * p.in[0].head_stride, m);
-        vv = load_row(v_src + h * p.in[1].head_stride, plain);
+    // the rows are on their way while the token's place is looked up
+    const int lane8 = lane % LANES * 8;
+    uint16_t *k_row = in_rows[warp] + lane / LANES * D, *v_row = k_row + UNIT_BYTES / 4;
+    for (int i = 0; h + i < h1; i += GROUP) {
+        copy16(k_row + i * D + lane8, k_src + (h + i) * p.in[0].head_stride + lane8);
+        copy16(v_row + i * D + lane8, v_src + (h + i) * p.in[1].head_stride + lane8);
     }
     const int b = warp_find_seq(p.batch, t, lane);
     bool bad = false;
@@ -300,6 +311,7 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) kv_append_kernel(const AppendP
     }
     if (bad && lane == 0)
         atomicOr(p.status, kStatusBadIndex);
+    copies_done();
     if (id < 0)
         return;  // the token belongs to no sequence, or has no place in the cache
     const int64_t row = pos & ((1 << p.batch.page_shift) - 1);
@@ -310,20 +322,16 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) kv_append_kernel(const AppendP
     if (p.half > 0)
         load_rotations(cs[warp], p.positions != nullptr ? __ldg(p.positions + t) : pos, p.inv_freq, p.half, m, lane, c, s);
     const float r0 = __frcp_rn(s0), r1 = __frcp_rn(s1);
-    for (int i = u * p.unit_heads; i < h1; i += GROUP, h += GROUP) {  // alike for all lanes
+    for (int i = u * p.unit_heads; i < h1; i += GROUP, h += GROUP, k_row += GROUP * D, v_row += GROUP * D) {  // alike for all lanes
         float x[8], y[8];
-        unpack8(kv, x);
-        unpack8(vv, y);
-        if (h + GROUP < h1) {
-            kv = load_row(k_src + (h + GROUP) * p.in[0].head_stride, m);
-            vv = load_row(v_src + (h + GROUP) * p.in[1].head_stride, plain);
-        }
+        unpack8(load_row(k_row, m), x);
+        unpack8(*reinterpret_cast<const uint4 *>(v_row + lane8), y);
         norm_rotate<D>(x, p.weight != nullptr, w, p.eps, m.turned, c, s);
         const uint2 kc = codes8(x, s0, r0), vc = codes8(y, s1, r1);
         if (h < h1) {
             *reinterpret_cast<uint32_t *>(k_dst + h * p.head_stride[0] + m.a) = kc.x;
             *reinterpret_cast<uint32_t *>(k_dst + h * p.head_stride[0] + m.b) = kc.y;
-            *reinterpret_cast<uint2 *>(v_dst + h * p.head_stride[1] + plain.a) = vc;
+            *reinterpret_cast<uint2 *>(v_dst + h * p.head_stride[1] + lane8) = vc;
         }
     }
 }
