@@ -457,10 +457,11 @@ size_t nvfp4_fp8_kv_attention_workspace_bytes(int64_t tokens, int64_t q_heads, i
  * receives max|out| over the rows written (bf16 magnitude bits, the form
  * NVFP4_AMAX_GIVEN takes).  out must not overlap q or gate.  q_heads is a
  * multiple of kv_heads, at most 128 times it.
- * Softmax statistics and sums are fp32; queries enter the FP8 MMA as the sum
- * of two E4M3 terms, which hold all 8 bits of a bf16 value (values below
- * 2^-10 of their row's largest lose low bits), probabilities as the sum of
- * two E4M3 terms of 8 bits together.  The order of the sums depends on the
+ * Softmax statistics and sums are fp32.  In tiles of several tokens queries
+ * enter the FP8 MMA as the sum of two E4M3 terms, which hold all 8 bits of a
+ * bf16 value (values below 2^-10 of their row's largest lose low bits),
+ * probabilities as the sum of two E4M3 terms of 8 bits together; for single
+ * tokens both are f16: queries exact, probabilities of 11 bits.  The order of the sums depends on the
  * lengths of the whole batch: the same call gives the same bits.
  * ws: nvfp4_fp8_kv_attention_workspace_bytes(...) bytes, 16-byte aligned,
  * scratch only: nothing is kept in it between calls. */

@@ -228,16 +228,35 @@ attn::Parts parts_at(uint8_t *base, int64_t rows)
     return p;
 }
 
-// Which kernels a call launches, and the cost of their items in keys.
-constexpr int32_t kMixedItems = 370, kPadRows = 8;
-constexpr int32_t kTileItemCost256 = 1152, kTileItemCost128 = 512, kDecodeItemCost = 128;
+// Where a batch may hold both kinds of sequences, the single tokens get their
+// own kernel beside the tile kernel from this many single items on (sequences
+// x key heads).  Measured (us, both kernels against the tile kernel alone):
+// 64 x 4 heads of 256, 8192 keys, one chunk of 512: 226 against 212; 16 x 4
+// with a chunk of 1000: 183 against 153; 200 x 4 with 2000 keys: 166 against
+// 187; 48 x 8 heads of 128, 4000 keys: 127 against 141; 128 x 8: 128 against
+// 169; 32 x 8: 60 against 59.
+constexpr int32_t kMixedItems = 370;
+// Rows beyond the sequences up to which a batch counts as padded single
+// tokens.  For single tokens alone (us, their kernel against the tile
+// kernel): 64 x 8192 keys of 4 heads of 256: 101 against 122; 64 x 500: 27
+// against 44; 1 x 777: 15.3 against 16.7; 256 x 1000 keys of 8 heads of 128:
+// 86 against 171.
+constexpr int32_t kPadRows = 8;
+// What an item costs beside its keys, in keys: the time from one item's last
+// block to the next one's first.  Tile kernel, D = 256: 20 thousand cycles (a
+// block of 128 keys: 2300 to 2600); a prompt of 8192 takes 866 us at 512 and
+// 815 at 1152.  Single tokens, D = 256: 64 x 8192 takes 107 us at 32, 105 at
+// 128, 101 at 320; D = 128: 256 x 1000 takes 101 at 32, 86 at 128, 93 at 320.
+constexpr int32_t kTileItemCost256 = 1152, kTileItemCost128 = 512, kDecodeItemCost256 = 320, kDecodeItemCost128 = 128;
 
-// Heads that one warp of the row kernels takes: one while the rows do not
-// fill the GPU, then as many as make a few warps for every place, up to
-// `most`, sharing the token's angles.
+// Heads that one warp of the row kernels takes, sharing the token's angles:
+// one while the rows do not fill the GPU, then as many as leave 16 warps an
+// SM, up to `most`.  Measured (us): 16 tokens x 28 heads 2.6 with one, 4.2
+// with 8; 1337 tokens 7.2 with 3, 5.2 with 8; 8192 tokens 62 with 2, 49 with
+// 4, 45 with 8.
 int unit_heads(int64_t rows, int64_t heads, int sm_count, int64_t most)
 {
-    return static_cast<int>(std::max<int64_t>(1, std::min({most, heads, rows / (int64_t(sm_count) * 64)})));
+    return static_cast<int>(std::max<int64_t>(1, std::min({most, heads, rows / (int64_t(sm_count) * 16)})));
 }
 
 int64_t row_blocks(int64_t units) { return cdiv(units, attn::ROW_WARPS); }
@@ -415,8 +434,9 @@ extern "C" int nvfp4_fp8_kv_attention(const nvfp4_heads *q, const nvfp4_heads *g
     // heads that share a key fit its rows.  The lengths are on the device, so
     // the sizes have to say which kernels may find work: as many token rows as
     // sequences or fewer, all go there (it is right for longer ones too, but
-    // reads their keys again for every token); a batch of some sequences, or
-    // one padded by a few rows, may hold both kinds; else it is prompts alone.
+    // reads their keys again for every token); a few rows more may be padding
+    // or a short chunk, and many sequences hold both kinds: both kernels; else
+    // the tile kernel takes everything.
     const int64_t group = q->heads / cache->kv_heads;
     const bool single = group <= attn::DECODE_ROWS &&
                         (int64_t(batch->num_seqs) * cache->kv_heads >= kMixedItems || tokens <= int64_t(batch->num_seqs) + kPadRows);
@@ -454,7 +474,7 @@ extern "C" int nvfp4_fp8_kv_attention(const nvfp4_heads *q, const nvfp4_heads *g
         p.tile_tokens = k == 0 ? attn::ROW_TILE / p.group : 1;
         p.batch.fresh_min = k == 0 && single ? 2 : 1;
         p.batch.fresh_max = k == 0 || !tiled ? INT32_MAX : 1;
-        p.batch.item_cost = k != 0 ? kDecodeItemCost : cache->head_dim == 256 ? kTileItemCost256 : kTileItemCost128;
+        p.batch.item_cost = cache->head_dim == 256 ? (k ? kDecodeItemCost256 : kTileItemCost256) : (k ? kDecodeItemCost128 : kTileItemCost128);
         if (k == 0)
             launch(cache->head_dim == 256 ? attn::paged_attention_kernel<256> : attn::paged_attention_kernel<128>,
                    dim3(attn::CTAS), dim3(attn::ATTN_THREADS),

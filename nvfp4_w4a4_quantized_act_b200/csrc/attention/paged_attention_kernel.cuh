@@ -30,7 +30,7 @@
 //
 // One CTA per SM; query tile of 128 rows (tokens x query heads of one key
 // head) against blocks of 128 keys; work is shared by attention_schedule.cuh.
-//   warp 0       loads K and V blocks page by page (4-D TMA, 128-byte
+//   warps 0, 3   load K blocks and V blocks page by page (4-D TMA, 128-byte
 //                swizzle) into a ring of stages
 //   warp 1       TMEM; one lane issues the MMAs: scores of block j+1 before
 //                the values of block j, so the softmax of one block runs under
@@ -43,7 +43,24 @@
 //                TMEM over the scores, queries to shared memory
 // The softmax of a block has the time of two products (2 x 1060 cycles at
 // D = 256) before the tensor cores would wait for it; everything that is not
-// on its path is done by other warps beside it.
+// on its path is done by other warps beside it.  An SM's quarter issues such
+// code at one instruction in two cycles, so instructions count, not units: a
+// block's 2 x 64 scores of a quarter take some 2250 cycles (350 for the
+// maximum, 300 for the reference, 2 x 800 for powers and terms), and powers
+// moved from the special-function unit to the FMA pipe made it slower.
+//
+// Measured (24 query heads on 4 key heads of 256): four chunks of 509 tokens
+// over histories to 16384, 354 GFLOP, 312 us, 1.13 PFLOP/s; a prompt of 8192,
+// 825 GFLOP, 815 us, 1.01 PFLOP/s, where the board's 1.63 for plain 16-bit
+// products is the measure.  A block takes 2300 to 2600 cycles, 2130 of them
+// on the tensor cores: the softmax bounds it.  From one item's last block to
+// the next one's first go 20 thousand cycles (8 rows of queries a warp split
+// into terms, and a row of results a lane, gated): at D = 256 the accumulator
+// and two blocks of scores fill TMEM, so nothing of the next item's values can
+// begin before.  Eight warps for the results in place of four, with fewer
+// registers for the softmax, gained nothing.  With K and V fetched by one warp that
+// read the page table block by block, the chunks took 551 thousand cycles a
+// CTA, now 454.
 // TMEM: D columns of output, two buffers of 128 score columns.  P of a block
 // replaces its scores: high and low terms, four keys per column.
 //

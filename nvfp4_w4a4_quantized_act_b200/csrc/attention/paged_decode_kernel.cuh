@@ -31,6 +31,13 @@
 // into the product's operand; a byte shuffle puts two keys of a dimension side
 // by side.  MMA row n stands for key n for even n and key ((n - 1) ^ 4) + 1 for
 // odd n, which makes both reads free of bank conflicts under the swizzle.
+//
+// Measured (24 query heads on 4 key heads of 256, parts joined): 64 sequences
+// of up to 8192 keys, 527 MB, 101 us, 5.2 TB/s; 2 of 131072, 537 MB, 99 us,
+// 5.4 TB/s (a copy on this board runs at 6.45).  A CTA's start (offsets, page
+// table, first keys: three loads that wait for one another), the join and the
+// launches take some 13 us of each; one sequence of 777 keys takes 15 us for
+// them alone.
 #pragma once
 
 #include <climits>

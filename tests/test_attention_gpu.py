@@ -98,6 +98,34 @@ def test_many_sequences(n_seqs):
     _run(c, 8, only=set(range(0, n_seqs, 7)) | set(range(n_seqs - 5, n_seqs)))
 
 
+@pytest.mark.parametrize("D,kv,n_seqs", [(256, 4, 91), (256, 4, 100), (128, 8, 46), (128, 8, 47), (256, 1, 370)])
+def test_single_tokens_beside_chunks(D, kv, n_seqs):
+    """Around the number of sequences from which the single tokens of a mixed
+    batch have a kernel of their own."""
+    seqs = [(1, 1 + (i * 61) % 400) for i in range(n_seqs)]
+    seqs[3], seqs[n_seqs // 2], seqs[-1] = (40, 390), (2, 2), (25, 130)
+    c = Cache(seqs, kv, D, 16, seed=n_seqs, tokens_pad=11)
+    fill_normal(c, 9)
+    _run(c, 4 * kv, only=set(range(0, n_seqs, 9)) | {3, n_seqs // 2, n_seqs - 1})
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("seqs", [[(1, 90)], [(1, 6000)], [(130, 300), (1, 40)], [(60, 5000)]])
+def test_gates_of_any_size(D, seqs):
+    """Single tokens and tiles, of one CTA and joined: gates that close, that
+    are infinite or no numbers."""
+    c = Cache(seqs, 1, D, 32, seed=D)
+    fill_normal(c, 2)
+    q, gate = _queries(c, 6, 31)
+    gate = gate * 4
+    for i, x in enumerate([float("inf"), float("-inf"), float("nan"), 60.0, -60.0, 90.0, -90.0, 1e4, -1e4, 3e38, -3e38, 0.0, -0.0]):
+        gate[..., i::41] = x
+    out = torch.empty(c.tokens, 6, D, dtype=torch.bfloat16, device=DEV)
+    ops.fp8_kv_attention(q, *c.args(), gate=gate, out=out)
+    assert ops.get_status() == 0
+    check_attention(c, q, gate, out, D ** -0.5)
+
+
 @pytest.mark.parametrize("D", [128, 256])
 def test_long_history(D):
     c = Cache([(1, 20011), (3, 9000)], 2, D, 64, seed=D)
