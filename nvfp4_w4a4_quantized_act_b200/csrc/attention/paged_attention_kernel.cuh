@@ -14,7 +14,7 @@
 //   [128, 256); high = E4M3(x), low = E4M3(x - high).  A bf16 value has 8
 //   significant bits, two E4M3 values 4 each: exact down to 2^-10 of the row's
 //   largest, off by at most 2^-17 of the largest below.
-//   Probabilities: 2^(t - r + 8); high keeps 4 significant bits by
+//   Probabilities: 2^(t - r + 8), in f16; high keeps 4 significant bits by
 //   truncation, low = E4M3(p - high): 8 bits together, as bf16 would keep, but
 //   no finer than 2^-9.  So the reference r has to keep the probabilities up:
 //   it follows the blocks of 128 keys both ways, not only up as a running
@@ -98,6 +98,7 @@ constexpr int STAGE_LD = 36;        // floats of a row of the results' staging: 
 constexpr uint64_t ATTN_WAIT_NS = 2000000000ull, ATTN_DRAIN_NS = 10000000ull;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr float P_SHIFT = 8.0f;       // probabilities are 2^(t - r + P_SHIFT)
+constexpr float P_UNIT = 256.0f;      // 2^P_SHIFT
 constexpr float REF_UP = 0.75f;       // 2^(P_SHIFT + REF_UP) < 448
 constexpr float REF_DOWN = 3.0f;
 constexpr float BLOCK_SUM = 32.0f;    // 2^(P_SHIFT - REF_DOWN): a block above that edge has it in its largest alone
@@ -909,7 +910,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
                 f = sm->row_scale[row] * c;
                 f = f < 1.17549435e-38f ? 1.17549435e-38f : f;  // keeps (-inf) * f; NaN stays
             }
-            const uint64_t ff = pack2(f, f), neg = pack2(-1.0f, -1.0f);
+            const uint64_t ff = pack2(f, f);
             uint64_t sum2 = 0;  // two fp32 sums
             float so_far = 0.0f;
 #pragma unroll 1
@@ -947,7 +948,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
                     const float tm = fmaxf(mine, other.x) * f;
                     // ref is -inf until the row has seen a key; one branch for the warp, few blocks take it
                     const bool up = tm > ref + REF_UP;
-                    const bool down = tm < ref - REF_DOWN && so_far + other.y < BLOCK_SUM * static_cast<float>(j) && tm > -INFINITY;
+                    const bool down = tm < ref - REF_DOWN && so_far + other.y < BLOCK_SUM / P_UNIT * static_cast<float>(j) && tm > -INFINITY;
                     top = fmaxf(top, tm);
                     if (__any_sync(0xFFFFFFFFu, up || down)) {
                         if (up || down) {
@@ -964,9 +965,13 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
                     if (lane == 0)
                         mbar_arrive(smem_u32(&sm->turn_ready[buf]));
                 }
-                const float shift = P_SHIFT - (ref > -INFINITY ? ref : 0.0f);
-                const uint64_t bb = pack2(shift, shift);
+                const float minus_ref = ref > -INFINITY ? -ref : 0.0f;
+                const uint64_t bb = pack2(minus_ref, minus_ref);
                 uint64_t sum_b = 0;
+                // A pair of probabilities goes to f16 (11 bits) without its 2^8.  There the byte below the sign holds the
+                // E4M3 code of 2^8 times the value cut to 4 bits, subnormal codes too: the high term; the rest,
+                // exact, is the low term rounded to nearest by half a step.  As conversions to E4M3 the two terms took
+                // 16 cycles more of every four scores'.
                 // Scores are read from TMEM a second time, 32 at a time, instead of being held: the loop's code is
                 // half as long, and the warps' loops together have to fit the instruction cache.
 #pragma unroll 1
@@ -977,18 +982,18 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
                         tc_wait_ld();
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
-                            uint64_t x[2], y[2], z[2];
+                            uint64_t x[2];
+                            uint32_t h[2], l[2];
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                const uint64_t t = fma2(pack2u(v[4 * k + 2 * e], v[4 * k + 2 * e + 1]), ff, bb);
-                                x[e] = exp2_fast2(t);
-                                y[e] = x[e] & 0xFFF00000FFF00000ull;
-                                z[e] = fma2(y[e], neg, x[e]);
+                                x[e] = exp2_fast2(fma2(pack2u(v[4 * k + 2 * e], v[4 * k + 2 * e + 1]), ff, bb));
+                                h[e] = f16x2_of(x[e]);
+                                l[e] = sub_f16x2(h[e], h[e] & 0x7F807F80u);
                             }
                             sum2 = add2(sum2, x[0]);
                             sum_b = add2(sum_b, x[1]);
-                            hi[k] = e4m3x4_of(y[0], y[1]);
-                            lo[k] = e4m3x4_of(z[0], z[1]);
+                            hi[k] = __byte_perm(h[0] << 1, h[1] << 1, 0x7531);
+                            lo[k] = __byte_perm((l[0] << 1) + 0x00800080u, (l[1] << 1) + 0x00800080u, 0x7531);
                         }
                         tc_st_32x32b_x8(scol + c32 * 8, hi);
                         tc_st_32x32b_x8(scol + 16 + c32 * 8, lo);
@@ -1004,7 +1009,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
                 unpack2(sum2, sa, sb);
                 so_far = sa + sb;
             }
-            sm->sum[i & 1][half][row] = so_far;
+            sm->sum[i & 1][half][row] = so_far * P_UNIT;
             if (half == 0)
                 sm->ref[i & 1][row] = top > -INFINITY ? ref : -INFINITY;
             __syncwarp();

@@ -102,19 +102,6 @@ __device__ __forceinline__ bool named_barrier_any(uint32_t id, uint32_t count, b
     return any != 0;
 }
 
-// Four E4M3 codes (round to nearest even, saturating at +-448), a in the low byte.
-__device__ __forceinline__ uint32_t f32_to_e4m3x4(float a, float b, float c, float d)
-{
-    uint32_t r;
-    asm("{\n\t.reg .b16 lo, hi;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
-        "mov.b32 %0, {lo, hi};\n\t}"
-        : "=r"(r)
-        : "f"(a), "f"(b), "f"(c), "f"(d));
-    return r;
-}
-
 // Two fp32 values in a register pair, and the packed arithmetic on them.
 __device__ __forceinline__ uint64_t pack2u(uint32_t lo, uint32_t hi)
 {
@@ -148,12 +135,21 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-__device__ __forceinline__ uint32_t e4m3x4_of(uint64_t ab, uint64_t cd)
+// A pair as two f16 values (round to nearest even), the first in the low half,
+// and the difference of two such words.
+__device__ __forceinline__ uint32_t f16x2_of(uint64_t ab)
 {
-    float a, b, c, d;
+    float a, b;
+    uint32_t r;
     unpack2(ab, a, b);
-    unpack2(cd, c, d);
-    return f32_to_e4m3x4(a, b, c, d);
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
 // 32 lanes x 8 consecutive 32-bit columns from registers.
