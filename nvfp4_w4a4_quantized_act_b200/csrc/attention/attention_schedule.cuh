@@ -143,6 +143,7 @@ struct WalkStart {
     int b, h, m;
     int64_t x, left;
     int64_t total;
+    SeqItems q;  // of sequence b
 };
 
 // Fills `st` (shared memory) with the start of CTA `cta` of CTAS; all THREADS
@@ -156,8 +157,8 @@ __device__ __forceinline__ void find_start(const BatchView &v, int kv_heads, int
     const int per = (v.num_seqs + THREADS - 1) / THREADS;
     const int b0 = min(tid * per, v.num_seqs), b1 = min(b0 + per, v.num_seqs);
     int64_t mine = 0;
+    SeqItems q;  // kept where the thread has one sequence alone
     for (int b = b0; b < b1; ++b) {
-        SeqItems q;
         q.set(load_seq(v, b, bad), v, tile_tokens);
         mine += q.total(tile_tokens) * kv_heads;
     }
@@ -172,7 +173,8 @@ __device__ __forceinline__ void find_start(const BatchView &v, int kv_heads, int
         scratch[warp] = scan;
     __syncthreads();
     int64_t base = 0, total = 0;
-    for (int w = 0; w < THREADS / 32; ++w) {
+    const int used = min(THREADS / 32, (v.num_seqs + 32 * per - 1) / (32 * per));  // warps with sequences
+    for (int w = 0; w < used; ++w) {
         base += w < warp ? scratch[w] : 0;
         total += scratch[w];
     }
@@ -184,8 +186,8 @@ __device__ __forceinline__ void find_start(const BatchView &v, int kv_heads, int
     }
     if (to > from && from >= at && from < at + mine) {
         for (int b = b0; b < b1; ++b) {
-            SeqItems q;
-            q.set(load_seq(v, b, bad), v, tile_tokens);
+            if (per > 1)
+                q.set(load_seq(v, b, bad), v, tile_tokens);
             const int64_t one = q.total(tile_tokens);
             if (from < at + one * kv_heads) {
                 int64_t off = from - at;
@@ -203,6 +205,7 @@ __device__ __forceinline__ void find_start(const BatchView &v, int kv_heads, int
                 }
                 st->m = lo;
                 st->x = off - q.before(lo, tile_tokens);
+                st->q = q;
                 break;
             }
             at += one * kv_heads;

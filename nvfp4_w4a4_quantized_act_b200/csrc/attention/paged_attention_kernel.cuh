@@ -578,10 +578,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
         walk.m = sm->start.m;
         walk.x = sm->start.x;
         walk.left = sm->start.left;
-        if (walk.left > 0) {
-            bool ignored = false;
-            walk.q.set(load_seq(p.batch, walk.b, ignored), p.batch, p.tile_tokens);
-        }
+        walk.q = sm->start.q;
         PartInfo info;
         info.continues = info.owns = 0;
         info.last = info.token0 = info.rows = info.group0 = info.past0 = info.pad = 0;
@@ -1037,32 +1034,47 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
 //
 // The bytes are few (D floats a part and row); what counts is how many loads
 // wait for one another and how many rows are in flight.  Once a row's item is
-// known, its gate, its parts' states and, where JOIN_AHEAD CTAs or fewer share
-// it, their sums are asked for at once, and 64 registers leave room for 32 warps on an SM: with
-// 107 and the loads one after the other the join of 148 x 126 rows of 256
-// took 33 us.
-constexpr int JOIN_ROWS = 8, JOIN_AHEAD = 4;
+// known, its gate and, where AHEAD CTAs or fewer share it, their sums are asked
+// for at once.  After tiles, AHEAD = 4 leaves room for 32 warps on an SM: with
+// 107 registers and the loads one after the other the join of 148 x 126 rows
+// of 256 took 33 us.  After single tokens alone there are few rows, and an
+// item may have many parts: AHEAD = 8.
+constexpr int JOIN_ROWS = 8;
 
-template <int D>
-__global__ void __launch_bounds__(JOIN_ROWS * 32, 4) paged_attention_join_kernel(const AttnParams p, const Parts second)
+template <int D, int AHEAD>
+__global__ void __launch_bounds__(JOIN_ROWS * 32, AHEAD > 4 ? 2 : 4) paged_attention_join_kernel(const AttnParams p, const Parts second)
 {
     grid_dep_wait();
     grid_dep_launch_dependents();
     const Parts parts = blockIdx.x < CTAS ? p.parts : second;
     const int cta = blockIdx.x % CTAS, lane = threadIdx.x & 31;
     const int row = blockIdx.y * JOIN_ROWS + (threadIdx.x >> 5);
+    if (row >= parts.rows)
+        return;
+    auto slot_of = [&](int c) { return (static_cast<int64_t>(c) * 2 + (c == cta ? 1 : 0)) * parts.rows + row; };
+    // A lane for every CTA of a span of 32: which hold a part, and their references and sums.  The first span's are
+    // asked for together with the row's item, before it is known how far that goes.
+    auto state = [&](int c, float2 &ml) {
+        ml = make_float2(-INFINITY, 0.0f);
+        if (c >= CTAS)
+            return false;
+        ml = *reinterpret_cast<const float2 *>(parts.ml + slot_of(c) * 2);
+        return c == cta || parts.info[c].continues != 0;
+    };
+    float2 ml;
+    bool has = state(cta + lane, ml);
     const PartInfo info = parts.info[cta];
     const float ks = __ldg(p.k_scale), vs = __ldg(p.v_scale);
     if (!info.owns || row >= info.rows || !valid_scale(ks) || !valid_scale(vs))
         return;
+    has = has && cta + lane <= info.last;
     constexpr int PER = D / 128;
     const int tk = row / p.group, h = info.group0 + row - tk * p.group;
-    auto slot_of = [&](int c) { return (static_cast<int64_t>(c) * 2 + (c == cta ? 1 : 0)) * parts.rows + row; };
-    int pick[JOIN_AHEAD];  // CTAs whose parts are in x, from the span's first; -1: none
-    float4 x[JOIN_AHEAD][PER];
+    int pick[AHEAD];  // CTAs whose parts are in x, from the span's first; -1: none
+    float4 x[AHEAD][PER];
     auto load = [&](int c0) {
 #pragma unroll
-        for (int e = 0; e < JOIN_AHEAD; ++e) {
+        for (int e = 0; e < AHEAD; ++e) {
             const float *src = parts.o + slot_of(c0 + max(pick[e], 0)) * D + lane * 4;
 #pragma unroll
             for (int i = 0; i < PER; ++i)
@@ -1070,22 +1082,12 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32, 4) paged_attention_join_kernel
                     x[e][i] = *reinterpret_cast<const float4 *>(src + i * 128);
         }
     };
-    // A lane for every CTA of a span of 32: which hold a part, and their references and sums
-    auto state = [&](int c, float2 &ml) {
-        ml = make_float2(-INFINITY, 0.0f);
-        if (c > info.last)
-            return false;
-        ml = *reinterpret_cast<const float2 *>(parts.ml + slot_of(c) * 2);
-        return c == cta || parts.info[c].continues != 0;
-    };
     uint2 gate[PER];
-    float2 ml;
-    bool has = state(cta + lane, ml);
     // Few CTAs: all their sums are read before it is known which of them hold a part
-    const bool near = info.last - cta < JOIN_AHEAD;
+    const bool near = info.last - cta < AHEAD;
     if (near) {
 #pragma unroll
-        for (int e = 0; e < JOIN_AHEAD; ++e)
+        for (int e = 0; e < AHEAD; ++e)
             pick[e] = cta + e <= info.last ? e : -1;
         load(cta);
     }
@@ -1095,7 +1097,7 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32, 4) paged_attention_join_kernel
     float top = has ? ml.x : -INFINITY;
     for (int c = cta + 32 + lane; c - lane <= info.last; c += 32) {
         float2 more;
-        if (state(c, more))
+        if (state(c, more) && c <= info.last)
             top = fmaxf(top, more.x);
     }
 #pragma unroll
@@ -1108,7 +1110,7 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32, 4) paged_attention_join_kernel
 #pragma unroll 1
     for (int c0 = cta; c0 <= info.last; c0 += 32) {
         if (c0 > cta)
-            has = state(c0 + lane, ml);
+            has = state(c0 + lane, ml) && c0 + lane <= info.last;
         uint32_t todo = __ballot_sync(0xFFFFFFFFu, has);
         const uint32_t there = todo;
         // no key in sight in any part: weight 1 keeps the zero or NaN sums
@@ -1119,14 +1121,14 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32, 4) paged_attention_join_kernel
                 todo = 0;
             } else {
 #pragma unroll
-                for (int e = 0; e < JOIN_AHEAD; ++e) {
+                for (int e = 0; e < AHEAD; ++e) {
                     pick[e] = todo ? __ffs(todo) - 1 : -1;
                     todo &= todo - 1;
                 }
                 load(c0);
             }
 #pragma unroll
-            for (int e = 0; e < JOIN_AHEAD; ++e) {
+            for (int e = 0; e < AHEAD; ++e) {
                 if (pick[e] < 0 || !(there >> pick[e] & 1u))
                     continue;
                 const float w = __shfl_sync(0xFFFFFFFFu, mine, pick[e]);

@@ -182,10 +182,7 @@ __global__ void __launch_bounds__(DECODE_THREADS, 1)
         walk.m = sm->start.m;
         walk.x = sm->start.x;
         walk.left = scales_ok ? sm->start.left : 0;
-        if (walk.left > 0) {
-            bool ignored = false;
-            walk.q.set(load_seq(p.batch, walk.b, ignored), p.batch, p.tile_tokens);
-        }
+        walk.q = sm->start.q;
         PartInfo info;
         info.continues = info.owns = 0;
         info.last = info.token0 = info.rows = info.group0 = info.past0 = info.pad = 0;

@@ -22,8 +22,10 @@ BUDGET = {
     "paged_attention_kernel<256>": (128, 8, 8),
     "paged_decode_kernel<128>": (168, 0, 0),
     "paged_decode_kernel<256>": (168, 40, 40),
-    "paged_attention_join_kernel<128>": (64, 0, 0),
-    "paged_attention_join_kernel<256>": (64, 0, 0),
+    "paged_attention_join_kernel<128, 4>": (64, 0, 0),
+    "paged_attention_join_kernel<256, 4>": (64, 0, 0),
+    "paged_attention_join_kernel<128, 8>": (128, 0, 0),
+    "paged_attention_join_kernel<256, 8>": (128, 0, 0),
 }
 
 
