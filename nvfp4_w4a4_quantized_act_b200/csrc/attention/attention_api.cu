@@ -487,11 +487,12 @@ extern "C" int nvfp4_fp8_kv_attention(const nvfp4_heads *q, const nvfp4_heads *g
         ++sets;
     }
     p.parts = parts[tiled ? 0 : 1];
-    const dim3 join_grid(static_cast<unsigned>(attn::CTAS * sets), static_cast<unsigned>(cdiv(p.parts.rows, attn::JOIN_ROWS)));
+    const int first_blocks = sets == 2 ? static_cast<int>(attn::CTAS * cdiv(parts[1].rows, attn::JOIN_ROWS)) : 0;
+    const dim3 join_grid(static_cast<unsigned>(first_blocks + attn::CTAS * cdiv(p.parts.rows, attn::JOIN_ROWS)));
     const bool wide = cache->head_dim == 256;
     launch(tiled ? (wide ? attn::paged_attention_join_kernel<256, 4> : attn::paged_attention_join_kernel<128, 4>)
                  : (wide ? attn::paged_attention_join_kernel<256, 8> : attn::paged_attention_join_kernel<128, 8>),
-           join_grid, dim3(attn::JOIN_ROWS * 32), 0, s, p, parts[1]);
+           join_grid, dim3(attn::JOIN_ROWS * 32), 0, s, p, parts[1], first_blocks);
     nvfp4::host::count_launch();
     return launch_ok();
 }

@@ -325,6 +325,22 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
     const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // uniform to the compiler too
     const int cta = blockIdx.x;
 
+    // Beside the kernel for single tokens this one may find nothing to do: a look at the offsets alone says so, before
+    // anything is set up, and the other kernel reports what is malformed.
+    if (p.batch.fresh_min > 1) {
+        grid_dep_wait();
+        bool some = false;
+        for (int b = tid; b < p.batch.num_seqs; b += ATTN_THREADS)
+            some |= __ldg(p.batch.cu + b + 1) - __ldg(p.batch.cu + b) >= p.batch.fresh_min;
+        if (__syncthreads_or(some) == 0) {
+            if (tid == 0) {
+                PartInfo none;
+                none.continues = none.owns = none.last = none.token0 = none.rows = none.group0 = none.past0 = none.pad = 0;
+                p.parts.info[cta] = none;
+            }
+            return;
+        }
+    }
     if (tid == 0) {
         for (int s = 0; s < A::STAGES; ++s) {
             mbar_init(smem_u32(&sm->full[s]), 1);
@@ -366,28 +382,17 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
 
     const float ks = __ldg(p.k_scale), vs = __ldg(p.v_scale);
     const bool scales_ok = valid_scale(ks) && valid_scale(vs);
-    // Beside the kernel for single tokens this one may find nothing to do: a look at the offsets alone says so, and
-    // the other kernel reports what is malformed.
-    bool idle = false;
-    if (p.batch.fresh_min > 1) {
-        bool some = false;
-        for (int b = tid; b < p.batch.num_seqs; b += ATTN_THREADS)
-            some |= __ldg(p.batch.cu + b + 1) - __ldg(p.batch.cu + b) >= p.batch.fresh_min;
-        idle = __syncthreads_or(some) == 0;
-    }
-    if (!idle) {
-        bool bad = false;
-        find_start<ATTN_THREADS>(p.batch, p.kv_heads, p.tile_tokens, cta, &sm->start, sm->scratch, bad);
-        if (cta == 0) {
-            if (!scales_ok && tid == 0)
-                atomicOr(p.status, kStatusNonFinite);
-            if (bad)
-                atomicOr(p.status, kStatusBadIndex);
-        }
+    bool bad = false;
+    find_start<ATTN_THREADS>(p.batch, p.kv_heads, p.tile_tokens, cta, &sm->start, sm->scratch, bad);
+    if (cta == 0) {
         if (!scales_ok && tid == 0)
-            sm->start.left = 0;
-        __syncthreads();
+            atomicOr(p.status, kStatusNonFinite);
+        if (bad)
+            atomicOr(p.status, kStatusBadIndex);
     }
+    if (!scales_ok && tid == 0)
+        sm->start.left = 0;
+    __syncthreads();
 
     // The next item, from warp 2; blocks = 0 at the end or when unwinding.
     auto take_item = [&](int i, bool &fail) -> Item {
@@ -400,13 +405,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
         return it;
     };
 
-    if (idle) {
-        if (tid == 0) {
-            PartInfo none;
-            none.continues = none.owns = none.last = none.token0 = none.rows = none.group0 = none.past0 = none.pad = 0;
-            p.parts.info[cta] = none;
-        }
-    } else if (warp == 0 || warp == 3) {
+    if (warp == 0 || warp == 3) {
         // ------------------------------------------------------ loads
         // Warp 0 fetches the K blocks, warp 3 the V blocks, into the ring in the order K0 K1 V0 K2 V1 .. K(n-1) V(n-2)
         // V(n-1).  A lane holds the page of one box, 32 boxes at a time and the next 32 on their way: read block by
@@ -1028,9 +1027,9 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
 
 // Joins the parts of the items that several CTAs worked on: CTA c's last
 // item, whose later parts are the first items of CTAs c+1 .. last.  One warp
-// per row; the parts are added in the order of their keys.  A second set of
-// parts (of the kernel for single tokens beside this one's) follows the first
-// in the grid.
+// per row; the parts are added in the order of their keys.  Where the
+// kernel for single tokens ran beside the tile kernel, its parts come first in
+// the grid: the tile kernel may have found nothing to do.
 //
 // The bytes are few (D floats a part and row); what counts is how many loads
 // wait for one another and how many rows are in flight.  Once a row's item is
@@ -1042,13 +1041,16 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
 constexpr int JOIN_ROWS = 8;
 
 template <int D, int AHEAD>
-__global__ void __launch_bounds__(JOIN_ROWS * 32, AHEAD > 4 ? 2 : 4) paged_attention_join_kernel(const AttnParams p, const Parts second)
+__global__ void __launch_bounds__(JOIN_ROWS * 32, AHEAD > 4 ? 2 : 4) paged_attention_join_kernel(const AttnParams p, const Parts first,
+                                                                                                    const int first_blocks)
 {
     grid_dep_wait();
     grid_dep_launch_dependents();
-    const Parts parts = blockIdx.x < CTAS ? p.parts : second;
-    const int cta = blockIdx.x % CTAS, lane = threadIdx.x & 31;
-    const int row = blockIdx.y * JOIN_ROWS + (threadIdx.x >> 5);
+    const bool other = static_cast<int>(blockIdx.x) < first_blocks;
+    const int block = static_cast<int>(blockIdx.x) - (other ? 0 : first_blocks);
+    const Parts parts = other ? first : p.parts;
+    const int cta = block % CTAS, lane = threadIdx.x & 31;
+    const int row = block / CTAS * JOIN_ROWS + (threadIdx.x >> 5);
     if (row >= parts.rows)
         return;
     auto slot_of = [&](int c) { return (static_cast<int64_t>(c) * 2 + (c == cta ? 1 : 0)) * parts.rows + row; };
