@@ -432,15 +432,17 @@ extern "C" int nvfp4_fp8_kv_attention(const nvfp4_heads *q, const nvfp4_heads *g
         return NVFP4_OK;
     // Sequences with one new token go to the kernel for single tokens where the
     // heads that share a key fit its rows.  The lengths are on the device, so
-    // the sizes have to say which kernels may find work: as many token rows as
-    // sequences or fewer, all go there (it is right for longer ones too, but
-    // reads their keys again for every token); a few rows more may be padding
-    // or a short chunk, and many sequences hold both kinds: both kernels; else
-    // the tile kernel takes everything.
+    // the sizes have to say which kernels may find work.  As many token rows as
+    // sequences: single tokens, padded or not, and all go there (it is right
+    // for longer ones too, but reads their keys again for every token).  Fewer
+    // rows, or a few more, may be single tokens or a chunk among sequences that
+    // stand still, and many sequences hold both kinds: both kernels, of which
+    // the tile kernel costs some 2 us when it finds nothing.  Else the tile
+    // kernel takes everything.
     const int64_t group = q->heads / cache->kv_heads;
     const bool single = group <= attn::DECODE_ROWS &&
                         (int64_t(batch->num_seqs) * cache->kv_heads >= kMixedItems || tokens <= int64_t(batch->num_seqs) + kPadRows);
-    const bool tiled = !single || tokens > batch->num_seqs;
+    const bool tiled = !single || tokens != batch->num_seqs;
     attn::AttnParams p;
     p.q = rows_of(q);
     p.gate = rows_of(gate);

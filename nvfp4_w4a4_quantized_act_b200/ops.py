@@ -20,7 +20,6 @@ LIB_PATH = os.path.join(_PKG, "libnvfp4.so")
 NVFP4_STATIC_SCALE = 1
 NVFP4_OUT_FP32 = 2
 NVFP4_AMAX_GIVEN = 4
-NVFP4_NORM_PLUS_ONE = 8
 NVFP4_DEBUG_INJECT_STALL = 1 << 30
 NVFP4_SINGLE_CTA = 1 << 29
 MAX_SEGMENTS = 16
@@ -51,33 +50,6 @@ class Nvfp4Error(RuntimeError):
 
 class Segment(ctypes.Structure):
     _fields_ = [("n_begin", ctypes.c_int64), ("n_end", ctypes.c_int64)]
-
-
-class Heads(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
-                ("heads", ctypes.c_int64)]
-
-
-class KvPages(ctypes.Structure):
-    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
-                ("v_scale", ctypes.c_void_p), ("k_page_stride", ctypes.c_int64), ("k_token_stride", ctypes.c_int64),
-                ("k_head_stride", ctypes.c_int64), ("v_page_stride", ctypes.c_int64),
-                ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64), ("num_pages", ctypes.c_int64),
-                ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
-
-
-class KvBatch(ctypes.Structure):
-    _fields_ = [("page_table", ctypes.c_void_p), ("cu_tokens", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
-                ("table_stride", ctypes.c_int64), ("num_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
-
-
-class NormRope(ctypes.Structure):
-    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p),
-                ("rotary_dim", ctypes.c_int32), ("eps", ctypes.c_float), ("flags", ctypes.c_uint)]
-
-
-class AttentionOpts(ctypes.Structure):
-    _fields_ = [("softmax_scale", ctypes.c_float), ("flags", ctypes.c_uint)]
 
 
 _lib = None

@@ -12,11 +12,39 @@ from nvfp4_w4a4_quantized_act_b200 import ops
 
 nbuild.build()
 
+# The host structs of include/nvfp4.h.
+class Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("heads", ctypes.c_int64)]
+
+
+class KvPages(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("k_page_stride", ctypes.c_int64), ("k_token_stride", ctypes.c_int64),
+                ("k_head_stride", ctypes.c_int64), ("v_page_stride", ctypes.c_int64),
+                ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64), ("num_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class KvBatch(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("cu_tokens", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("num_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
+class NormRope(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p),
+                ("rotary_dim", ctypes.c_int32), ("eps", ctypes.c_float), ("flags", ctypes.c_uint)]
+
+
+class AttentionOpts(ctypes.Structure):
+    _fields_ = [("softmax_scale", ctypes.c_float), ("flags", ctypes.c_uint)]
+
+
 FAKE = 1 << 20  # aligned, never dereferenced: checks fail first
 
 
 def _heads(heads=4, data=FAKE, st=1024, sh=256):
-    return ops.Heads(data, st, sh, heads)
+    return Heads(data, st, sh, heads)
 
 
 def _pages(**kw):
@@ -24,19 +52,19 @@ def _pages(**kw):
              k_head_stride=256, v_page_stride=16384, v_token_stride=1024, v_head_stride=256, num_pages=8, page_size=16,
              kv_heads=4, head_dim=256)
     v.update(kw)
-    return ops.KvPages(**v)
+    return KvPages(**v)
 
 
 def _batch(**kw):
     v = dict(page_table=FAKE, cu_tokens=FAKE, seq_lens=FAKE, table_stride=8, num_seqs=2, max_pages=8)
     v.update(kw)
-    return ops.KvBatch(**v)
+    return KvBatch(**v)
 
 
 def _nr(**kw):
     v = dict(q_weight=FAKE, k_weight=FAKE, inv_freq=FAKE, rotary_dim=64, eps=1e-6, flags=0)
     v.update(kw)
-    return ops.NormRope(**v)
+    return NormRope(**v)
 
 
 def _ref(x):
@@ -53,7 +81,7 @@ def append(k=_heads(), v=_heads(), tokens=3, pages=_pages(), batch=_batch(), pos
 
 def attend(q=_heads(24), gate=None, out=_heads(24), tokens=3, pages=_pages(), batch=_batch(), scale=0.1, flags=0, amax=None,
            ws=FAKE, ws_bytes=1 << 30, opts=True):
-    o = ops.AttentionOpts(scale, flags) if opts else None
+    o = AttentionOpts(scale, flags) if opts else None
     return ops.lib().nvfp4_fp8_kv_attention(_ref(q), _ref(gate), _ref(out), tokens, _ref(pages), _ref(batch), _ref(o), amax,
                                             ws, ws_bytes, None)
 
@@ -143,10 +171,10 @@ class _Recorder:
     that each is given."""
     NAMES = ("nvfp4_qk_norm_rope", "nvfp4_fp8_kv_append", "nvfp4_fp8_kv_attention")
     STRUCTS = {
-        "nvfp4_qk_norm_rope": ((0, ops.Heads), (1, ops.Heads), (2, ops.Heads), (3, ops.Heads), (7, ops.NormRope)),
-        "nvfp4_fp8_kv_append": ((0, ops.Heads), (1, ops.Heads), (3, ops.KvPages), (4, ops.KvBatch), (6, ops.NormRope)),
-        "nvfp4_fp8_kv_attention": ((0, ops.Heads), (1, ops.Heads), (2, ops.Heads), (4, ops.KvPages), (5, ops.KvBatch),
-                                   (6, ops.AttentionOpts)),
+        "nvfp4_qk_norm_rope": ((0, Heads), (1, Heads), (2, Heads), (3, Heads), (7, NormRope)),
+        "nvfp4_fp8_kv_append": ((0, Heads), (1, Heads), (3, KvPages), (4, KvBatch), (6, NormRope)),
+        "nvfp4_fp8_kv_attention": ((0, Heads), (1, Heads), (2, Heads), (4, KvPages), (5, KvBatch),
+                                   (6, AttentionOpts)),
     }
 
     def __init__(self):

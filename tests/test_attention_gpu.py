@@ -110,6 +110,18 @@ def test_single_tokens_beside_chunks(D, kv, n_seqs):
 
 
 @pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("new", [1, 20, 40])
+def test_sequences_that_stand_still(D, new):
+    """Fewer rows than sequences: a chunk or single tokens among sequences
+    without new tokens, in one kernel's hands or both's."""
+    seqs = [(0, 50 + i) for i in range(40)]
+    seqs[7], seqs[30] = (new, 700), (1, 300)
+    c = Cache(seqs, 2, D, 32, seed=new)
+    fill_normal(c, 5)
+    _run(c, 12)
+
+
+@pytest.mark.parametrize("D", [128, 256])
 @pytest.mark.parametrize("seqs", [[(1, 90)], [(1, 6000)], [(130, 300), (1, 40)], [(60, 5000)]])
 def test_gates_of_any_size(D, seqs):
     """Single tokens and tiles, of one CTA and joined: gates that close, that
