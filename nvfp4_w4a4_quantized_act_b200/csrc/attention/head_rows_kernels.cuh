@@ -300,9 +300,9 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) kv_append_kernel(const AppendP
         copy16(k_row + i * D + lane8, k_src + (h + i) * p.in[0].head_stride + lane8);
         copy16(v_row + i * D + lane8, v_src + (h + i) * p.in[1].head_stride + lane8);
     }
-    const int b = warp_find_seq(p.batch, t, lane);
+    int b;
     bool bad = false;
-    const Seq seq = load_seq(p.batch, b, bad);
+    const Seq seq = warp_find_seq(p.batch, t, lane, b, bad);
     const int j = t - seq.first, pos = seq.len - seq.fresh + j;
     int64_t id = -1;
     if (j >= 0 && j < seq.fresh && pos >= 0) {

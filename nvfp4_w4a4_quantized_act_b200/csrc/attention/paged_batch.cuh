@@ -32,11 +32,10 @@ struct Seq {
     int32_t first, fresh, len;
 };
 
-// Sequence b with its offsets clamped to the call's rows and its length to
-// the table's pages; `bad` is set when a clamp changed something.
-__device__ __forceinline__ Seq load_seq(const BatchView &v, int b, bool &bad)
+// Sequence b with its offsets (c0, c1) clamped to the call's rows and its
+// length n to the table's pages; `bad` is set when a clamp changed something.
+__device__ __forceinline__ Seq clamp_seq(const BatchView &v, int b, int32_t c0, int32_t c1, int32_t n, bool &bad)
 {
-    const int32_t c0 = __ldg(v.cu + b), c1 = __ldg(v.cu + b + 1), n = __ldg(v.lens + b);
     const int64_t cap = static_cast<int64_t>(v.max_pages) << v.page_shift;
     Seq s;
     s.first = min(max(c0, 0), v.tokens);
@@ -46,22 +45,36 @@ __device__ __forceinline__ Seq load_seq(const BatchView &v, int b, bool &bad)
     return s;
 }
 
+__device__ __forceinline__ Seq load_seq(const BatchView &v, int b, bool &bad)
+{
+    return clamp_seq(v, b, __ldg(v.cu + b), __ldg(v.cu + b + 1), __ldg(v.lens + b), bad);
+}
+
 // Last sequence b with cu[b] <= t (t < cu[num_seqs]), found by the 32 lanes
-// of a warp together: each round narrows the range to one of 32 parts.
-__device__ __forceinline__ int warp_find_seq(const BatchView &v, int32_t t, int lane)
+// of a warp together: each round narrows the range to one of 32 parts, and in
+// the last one every lane has what load_seq() reads of its sequence already.
+__device__ __forceinline__ Seq warp_find_seq(const BatchView &v, int32_t t, int lane, int &b, bool &bad)
 {
     int lo = 0, n = v.num_seqs;  // the answer lies in [lo, lo + n)
-    while (n > 1) {
+    // offsets ascend, so the lanes that hold form a prefix; lane 0 may miss only on malformed offsets
+    while (n > 32) {
         const int step = (n + 31) >> 5;
         const int at = lane * step;
-        const bool le = at < n && __ldg(v.cu + lo + at) <= t;
-        const uint32_t m = __ballot_sync(0xFFFFFFFFu, le);
-        // offsets ascend, so the lanes that hold form a prefix; lane 0 may miss only on malformed offsets
+        const uint32_t m = __ballot_sync(0xFFFFFFFFu, at < n && __ldg(v.cu + lo + at) <= t);
         const int k = m ? 31 - __clz(m) : 0;
         lo += k * step;
         n = min(step, n - k * step);
     }
-    return lo;
+    int32_t c0 = 0, c1 = 0, len = 0;
+    if (lane < n) {
+        c0 = __ldg(v.cu + lo + lane);
+        c1 = __ldg(v.cu + lo + lane + 1);
+        len = __ldg(v.lens + lo + lane);
+    }
+    const uint32_t m = __ballot_sync(0xFFFFFFFFu, lane < n && c0 <= t);
+    const int k = m ? 31 - __clz(m) : 0;
+    b = lo + k;
+    return clamp_seq(v, b, __shfl_sync(0xFFFFFFFFu, c0, k), __shfl_sync(0xFFFFFFFFu, c1, k), __shfl_sync(0xFFFFFFFFu, len, k), bad);
 }
 
 }  // namespace attn
