@@ -329,6 +329,9 @@ PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t n)
         if (gate != nullptr)
             hg = c.heads(*gate, "gate", &q);
         const nvfp4_heads ho = c.heads(out, "out", &q, true);
+        // CTAs read an item's queries while others write its results
+        if (out.numel() > 0 && (ho.data == hq.data || ho.data == hg.data))
+            refuse("out", "must not be q or the gate", out);
         if (!ws.is_contiguous())
             refuse("ws", "must be contiguous", ws);
         if (ws.nbytes() < g.attend_bytes(q.size(0), hq.heads, pages.kv_heads, q.size(2)))

@@ -582,9 +582,9 @@ def fp8_kv_attention(q, k_pages, v_pages, k_scale, v_scale, page_table, cu_token
                      gate=None, out=None, out_amax=None, ws=None, stream=None):
     """nvfp4_fp8_kv_attention -> out: causal attention of the batch's new
     tokens, q bf16 [tokens, q_heads, head_dim], over their sequences' pages,
-    times sigmoid(gate).  softmax_scale defaults to head_dim ** -0.5; out_amax
-    (4 bytes, e.g. the first word of a quantize workspace) receives max|out|
-    for quantize_act(..., amax_given=True)."""
+    times sigmoid(gate); out must not overlap q or gate.  softmax_scale defaults
+    to head_dim ** -0.5; out_amax (4 bytes, e.g. the first word of a quantize
+    workspace) receives max|out| for quantize_act(..., amax_given=True)."""
     if out is None:
         out = _new(stream, q.shape, torch.bfloat16, q.device)
     if ws is None:

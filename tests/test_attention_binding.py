@@ -210,6 +210,7 @@ bf16, i32 = torch.bfloat16, torch.int32
 Q, K = torch.zeros(3, 24, 256, dtype=bf16), torch.zeros(3, 4, 256, dtype=bf16)
 P = torch.zeros(8, 16, 4, 256, dtype=torch.uint8)
 ONE = torch.ones(1)
+G = torch.zeros_like(Q)
 TABLE, CU, LENS = torch.zeros(2, 4, dtype=i32), torch.tensor([0, 1, 3], dtype=i32), torch.tensor([5, 9], dtype=i32)
 F, W = torch.ones(32), torch.ones(256, dtype=bf16)
 POS = torch.zeros(3, dtype=i32)
@@ -268,6 +269,8 @@ BAD = {
     "attend: gate shape": lambda: ops.fp8_kv_attention(Q, *_cache(), gate=Q[:2]),
     "attend: out dtype": lambda: ops.fp8_kv_attention(Q, *_cache(), out=Q.float()),
     "attend: out overlaps itself": lambda: ops.fp8_kv_attention(Q, *_cache(), out=torch.zeros(3, 1, 256, dtype=bf16).expand(3, 24, 256)),
+    "attend: out is q": lambda: ops.fp8_kv_attention(Q, *_cache(), out=Q),
+    "attend: out is the gate": lambda: ops.fp8_kv_attention(Q, *_cache(), gate=G, out=G),
     "attend: small workspace": lambda: ops.fp8_kv_attention(Q, *_cache(), ws=torch.zeros(16, dtype=torch.uint8)),
     "attend: strided workspace": lambda: ops.fp8_kv_attention(Q, *_cache(), ws=torch.zeros(1 << 27, dtype=torch.uint8)[::2]),
     "norm: not a tensor": lambda: ops.qk_norm_rope(Q, None, [0, 1, 2], F),
