@@ -33,6 +33,13 @@ def test_norm_rope(T, Hq, Hk, D, rot, plus):
         check(o, ref, BF16 * ref.abs() + NORM_ROPE_U * size + 1e-37, f"T={T}")
 
 
+@pytest.mark.parametrize("T,Hq,Hk,D,rot", [
+    (1500, 24, 4, 256, 64), (2900, 17, 3, 128, 128), (700, 19, 2, 256, 96), (3100, 33, 1, 128, 16), (400, 9, 9, 256, 0)])
+def test_norm_rope_with_several_heads_a_warp(T, Hq, Hk, D, rot):
+    """Long batches: a warp takes up to 8 heads (16 of 128), the last fewer."""
+    test_norm_rope(T, Hq, Hk, D, rot, T % 200 == 0)
+
+
 def test_no_norm_and_one_side_only():
     g = gen(3)
     q = torch.randn(9, 4, 256, generator=g, device=DEV).to(torch.bfloat16)
@@ -125,6 +132,12 @@ def test_append(seqs, heads, D, page, rot, layout):
         assert torch.equal(c.v_pages[at].reshape(new, -1), codes)
     assert torch.equal(c.k_pages[~touched], before[0][~touched])
     assert torch.equal(c.v_pages[~touched], before[1][~touched])
+
+
+@pytest.mark.parametrize("seqs,heads,D", [
+    ([(1300, 1300), (900, 1000)], 6, 256), ([(1500, 1600), (0, 9), (1100, 1100)], 11, 128), ([(2500, 2500)], 5, 256)])
+def test_append_with_several_heads_a_warp(seqs, heads, D):
+    test_append(seqs, heads, D, 64, 64, "HND")
 
 
 def test_append_positions_given_and_negative_cache_positions():
