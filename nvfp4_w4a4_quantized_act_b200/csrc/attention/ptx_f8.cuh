@@ -174,6 +174,12 @@ __device__ __forceinline__ __half2 e4m3x2_to_f16x2(uint32_t v)
     return *reinterpret_cast<__half2 *>(&r);
 }
 
+// Two E4M3 codes of 2^8 times two f16 values below 1 (the product is exact).
+__device__ __forceinline__ uint32_t e4m3x2_of_rest(uint32_t x)
+{
+    return f16x2_to_e4m3x2(__hmul2(*reinterpret_cast<__half2 *>(&x), __float2half2_rn(256.0f)));
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float r;
