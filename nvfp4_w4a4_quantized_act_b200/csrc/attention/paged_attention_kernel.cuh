@@ -168,7 +168,10 @@ struct AttnSmem {
     int64_t scratch[ATTN_THREADS / 32];
     float2 red[2][2][ROW_TILE];    // by block parity: each half row's maximum, and its sum so far
     float turn[2][ROW_TILE];       // factor of the accumulated row before this block, by block parity
-    float row_scale[ROW_TILE];     // 1 / (power of two of the query row); NaN: the row is not finite
+    // By item parity, 1 / (power of two of the query row); NaN: the row is not finite.  A warp writes rows of every
+    // quarter and reads its own after barrier 5; after an item of a block or two it may write the next item's while
+    // another quarter has not read this one's, but it cannot pass the next item's barrier 5 before that.
+    float row_scale[2][ROW_TILE];
     float sum[2][2][ROW_TILE];     // by item parity: each half row's sum
     float ref[2][ROW_TILE];        // and the row's reference; -inf: no key seen
     int32_t nan_any[2];            // by item parity
@@ -886,7 +889,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
                         *reinterpret_cast<uint2 *>(at) = hi;
                         *reinterpret_cast<uint2 *>(at + A::SUBS * A::SUB_BYTES) = lo;
                         if ((lane % LANES) == 0)
-                            sm->row_scale[r] = unscale;
+                            sm->row_scale[i & 1][r] = unscale;
                         v[e] = next[e];
                     }
                 }
@@ -903,7 +906,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
             int vis = live ? max(it.past0 + static_cast<int>(row * p.group_inv >> 16) + 1, 0) - it.t0 * KEY_BLOCK - half * 64 : INT_MAX;
             float f = 0.0f, ref = -INFINITY, top = -INFINITY;
             if (live) {
-                f = sm->row_scale[row] * c;
+                f = sm->row_scale[i & 1][row] * c;
                 f = f < 1.17549435e-38f ? 1.17549435e-38f : f;  // keeps (-inf) * f; NaN stays
             }
             const uint64_t ff = pack2(f, f);
