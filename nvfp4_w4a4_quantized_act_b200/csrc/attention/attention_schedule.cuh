@@ -69,6 +69,16 @@ struct Item {
     int32_t head;        // key head
     int32_t seq;
     int32_t part;        // 0: the item is this CTA's alone; 1: begun by an earlier CTA; 2: finished by later ones
+
+    // No work and nothing to address: the end of a CTA's items, and what a warp goes on with when its wait for one
+    // ran out.
+    __host__ __device__ static Item none()
+    {
+        Item it;
+        it.blocks = it.t0 = it.keys = it.seen_first = it.rows = it.past0 = it.token0 = it.head = it.seq = 0;
+        it.part = 1;
+        return it;
+    }
 };
 
 // A CTA's walk over its part of the line.
@@ -88,12 +98,11 @@ struct Walk {
     int64_t left;  // cost left
     SeqItems q;
 
-    // The next item with key blocks for this CTA; blocks = 0 at the end.  `end_cost`: for part 2, the cost of the
+    // The next item with key blocks for this CTA; Item::none() at the end.  `end_cost`: for part 2, the cost of the
     // item behind this CTA's share.
     __device__ __forceinline__ Item next(const BatchView &v, int kv_heads, int tile_tokens, int group, int64_t &end_cost)
     {
         Item it;
-        it.blocks = 0;
         while (left > 0) {
             if (m >= q.tiles) {
                 m = 0;
@@ -104,7 +113,7 @@ struct Walk {
                     do {
                         if (++b >= v.num_seqs) {
                             left = 0;
-                            return it;
+                            return Item::none();
                         }
                         q.set(load_seq(v, b, ignored), v, tile_tokens);
                     } while (q.tiles == 0);
@@ -135,7 +144,7 @@ struct Walk {
                 return it;
             }
         }
-        return it;
+        return Item::none();
     }
 };
 

@@ -397,15 +397,16 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
         sm->start.left = 0;
     __syncthreads();
 
-    // The next item, from warp 2; blocks = 0 at the end or when unwinding.
-    auto take_item = [&](int i, bool &fail) -> Item {
-        Item it;
-        it.blocks = 0;
-        if (!fail && mbar_wait(smem_u32(&sm->item_ready[i % ITEMS]), (i / ITEMS) & 1, ATTN_WAIT_NS))
-            it = sm->items[i % ITEMS];
-        else
-            fail = true;
-        return it;
+    // The next item, from warp 2; Item::none() at the end and when unwinding.  `fail`: whether a wait of this
+    // thread, or with warp_item() of its warp, has run out.
+    auto thread_item = [&](int i, bool &fail) -> Item {
+        fail = fail || !mbar_wait(smem_u32(&sm->item_ready[i % ITEMS]), (i / ITEMS) & 1, ATTN_WAIT_NS);
+        return fail ? Item::none() : sm->items[i % ITEMS];
+    };
+    auto warp_item = [&](int i, bool &fail) -> Item {
+        fail = fail || !mbar_wait(smem_u32(&sm->item_ready[i % ITEMS]), (i / ITEMS) & 1, ATTN_WAIT_NS);
+        fail = __any_sync(0xFFFFFFFFu, fail);
+        return fail ? Item::none() : sm->items[i % ITEMS];
     };
 
     if (warp == 0 || warp == 3) {
@@ -423,8 +424,8 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
         bool fail = false, out_of_pool = false;
         uint32_t filled = 0, phases = 0;  // stages that this warp has filled, and the last time's phases
         for (int i = 0;; ++i) {
-            const Item it = take_item(i, fail);
-            if (!__all_sync(0xFFFFFFFFu, !fail) || it.blocks == 0)
+            const Item it = warp_item(i, fail);
+            if (it.blocks == 0)
                 break;
             const int32_t *table = p.batch.table + it.seq * p.batch.table_stride;
             const int box0 = it.t0 << boxes_shift, box1 = min((it.t0 + it.blocks) << boxes_shift, (it.keys + rows - 1) >> row_shift);
@@ -497,8 +498,8 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
                 fail = fail || !mbar_wait(smem_u32(&bar), phase & 1u, ATTN_WAIT_NS);
             };
             for (int i = 0;; ++i) {
-                const Item it = take_item(i, fail);
-                if (fail || it.blocks == 0)
+                const Item it = thread_item(i, fail);
+                if (it.blocks == 0)
                     break;
                 wait(sm->q_ready, i);
                 wait(sm->full[uses % A::STAGES], uses / A::STAGES);
@@ -647,11 +648,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
         // i - 2 is done, and block i + 2 waits for these warps.
         auto wait_values = [&](uint32_t i) { wait(sm->pv_done[i & 1], i >> 1); };
         for (int i = 0;; ++i) {
-            const Item it = take_item(i, fail);
-            if (__any_sync(0xFFFFFFFFu, fail))
-                fail = true;
-            if (!fail && it.blocks == 0)
-                break;
+            const Item it = warp_item(i, fail);
             const int ip = i & 1;
             const bool live = row < it.rows;
             // keys in this row's sight
@@ -741,11 +738,14 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
                         gv[e] = *reinterpret_cast<const uint4 *>(gate_at[e] + col);
             };
             load_gate(0);
-            wait(sm->stats_ready, i);
-            if (it.blocks > 0)
+            if (it.blocks > 0) {
+                wait(sm->stats_ready, i);
                 wait_values(block - 1);
-            fail = named_barrier_any(6, 128, fail);  // NaN marks are written
-            if (fail)
+            }
+            // NaN marks are written.  The vote is taken at the end marker too: a warp whose wait ran out comes here
+            // whatever the others were given, and none may leave before it has.
+            fail = named_barrier_any(6, 128, fail);
+            if (fail || it.blocks == 0)
                 break;
             tc_fence_after();
             const float total = sm->sum[ip][0][row] + sm->sum[ip][1][row];
@@ -855,12 +855,10 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
         uint32_t block = 0;
         bool fail = false;  // a wait of this thread ran out: no more waits until the item's vote makes it everyone's
         for (int i = 0;; ++i) {
-            const Item it = take_item(i, fail);
-            if (!fail && it.blocks == 0)
-                break;
+            const Item it = warp_item(i, fail);
             // Queries to shared memory as two E4M3 terms (the score MMAs of the item before have completed): each
             // warp takes every 8th row, or pair of rows, eight rows at a time and the other eight on their way
-            {
+            if (it.blocks > 0) {
                 constexpr int LANES = D / 8, GROUP = 32 / LANES, BATCH = 8 / GROUP;
                 const int col = (lane % LANES) * 8;
                 const uint16_t *src = p.q.data + it.token0 * p.q.token_stride + it.head * p.group * p.q.head_stride + col;
@@ -876,7 +874,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
                 uint4 v[BATCH];
                 load(sw * GROUP, v);
 #pragma unroll 1
-                for (int r0 = sw * GROUP; r0 < it.rows && !fail; r0 += 8 * GROUP * BATCH) {
+                for (int r0 = sw * GROUP; r0 < it.rows; r0 += 8 * GROUP * BATCH) {
                     uint4 next[BATCH];
                     load(r0 + 8 * GROUP * BATCH, next);
 #pragma unroll
@@ -898,8 +896,9 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
                 if (lane == 0)
                     mbar_arrive(smem_u32(&sm->q_ready));
             }
-            fail = named_barrier_any(5, SOFT_THREADS, fail);  // row_scale of this item is written
-            if (fail)
+            // row_scale of this item is written; a vote at the end marker too, as among the row warps
+            fail = named_barrier_any(5, SOFT_THREADS, fail);
+            if (fail || it.blocks == 0)
                 break;
             const bool live = row < it.rows, warp_live = quarter * 32 < it.rows;
             // keys in sight of this half row, from the current block's first; rows that no token fills need no mask
