@@ -24,7 +24,14 @@ namespace attn = nvfp4::attn;
 inline bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-int launch_ok() { return nvfp4::host::launch_failed() ? NVFP4_ERR_CUDA : NVFP4_OK; }
+// Status of a call whose last launch this was, which is counted if it took place.
+int launched()
+{
+    if (nvfp4::host::launch_failed())
+        return NVFP4_ERR_CUDA;
+    nvfp4::host::count_launch();
+    return NVFP4_OK;
+}
 
 int check_head_dim(int64_t d) { return (d == 128 || d == 256) ? NVFP4_OK : NVFP4_ERR_UNSUPPORTED_SHAPE; }
 
@@ -317,8 +324,7 @@ extern "C" int nvfp4_qk_norm_rope(const nvfp4_heads *q, const nvfp4_heads *k, co
     const dim3 grid(static_cast<unsigned>(row_blocks(tokens * (p.units[0] + p.units[1]))));
     launch(head_dim == 256 ? attn::qk_norm_rope_kernel<256> : attn::qk_norm_rope_kernel<128>, grid,
            dim3(attn::ROW_WARPS * 32), 0, static_cast<cudaStream_t>(stream), p);
-    nvfp4::host::count_launch();
-    return launch_ok();
+    return launched();
 }
 
 extern "C" int nvfp4_fp8_kv_append(const nvfp4_heads *k, const nvfp4_heads *v, int64_t tokens,
@@ -375,8 +381,7 @@ extern "C" int nvfp4_fp8_kv_append(const nvfp4_heads *k, const nvfp4_heads *v, i
     const dim3 grid(static_cast<unsigned>(row_blocks(tokens * p.units)));
     launch(cache->head_dim == 256 ? attn::kv_append_kernel<256> : attn::kv_append_kernel<128>, grid,
            dim3(attn::ROW_WARPS * 32), 0, static_cast<cudaStream_t>(stream), p);
-    nvfp4::host::count_launch();
-    return launch_ok();
+    return launched();
 }
 
 extern "C" size_t nvfp4_fp8_kv_attention_workspace_bytes(int64_t tokens, int64_t q_heads, int64_t kv_heads,
@@ -485,6 +490,9 @@ extern "C" int nvfp4_fp8_kv_attention(const nvfp4_heads *q, const nvfp4_heads *g
             launch(cache->head_dim == 256 ? attn::paged_decode_kernel<256> : attn::paged_decode_kernel<128>,
                    dim3(attn::CTAS), dim3(attn::DECODE_THREADS),
                    cache->head_dim == 256 ? attn::decode_smem_bytes<256>() : attn::decode_smem_bytes<128>(), s, tm_k, tm_v, p);
+        // The join takes addresses from what these kernels leave in the workspace: refused, they leave anything.
+        if (nvfp4::host::launch_failed())
+            return NVFP4_ERR_CUDA;
         nvfp4::host::count_launch();
         ++sets;
     }
@@ -495,6 +503,5 @@ extern "C" int nvfp4_fp8_kv_attention(const nvfp4_heads *q, const nvfp4_heads *g
     launch(tiled ? (wide ? attn::paged_attention_join_kernel<256, 4> : attn::paged_attention_join_kernel<128, 4>)
                  : (wide ? attn::paged_attention_join_kernel<256, 8> : attn::paged_attention_join_kernel<128, 8>),
            join_grid, dim3(attn::JOIN_ROWS * 32), 0, s, p, parts[1], first_blocks);
-    nvfp4::host::count_launch();
-    return launch_ok();
+    return launched();
 }

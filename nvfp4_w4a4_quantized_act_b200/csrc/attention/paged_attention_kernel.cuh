@@ -1070,11 +1070,14 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32, AHEAD > 4 ? 2 : 4) paged_atten
     bool has = state(cta + lane, ml);
     const PartInfo info = parts.info[cta];
     const float ks = __ldg(p.k_scale), vs = __ldg(p.v_scale);
-    if (!info.owns || row >= info.rows || !valid_scale(ks) || !valid_scale(vs))
+    // addresses come from the workspace: another call that uses it at the same time must not make them point elsewhere
+    const int tk = row / p.group, h = info.group0 + row - tk * p.group;
+    const bool outside = (static_cast<uint32_t>(info.last) >= CTAS) | (static_cast<uint32_t>(h) >= static_cast<uint32_t>(p.out.heads)) |
+                         (static_cast<uint32_t>(info.token0 + tk) >= static_cast<uint32_t>(p.batch.tokens));
+    if ((info.owns == 0) | (row >= info.rows) | outside | !valid_scale(ks) | !valid_scale(vs))
         return;
     has = has && cta + lane <= info.last;
     constexpr int PER = D / 128;
-    const int tk = row / p.group, h = info.group0 + row - tk * p.group;
     int pick[AHEAD];  // CTAs whose parts are in x, from the span's first; -1: none
     float4 x[AHEAD][PER];
     auto load = [&](int c0) {
