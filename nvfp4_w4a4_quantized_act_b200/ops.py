@@ -537,10 +537,19 @@ def _attention():
 
 def _new(stream, shape, dtype, device):
     """An output or scratch tensor for a call on `stream` (None: the current
-    one); the allocator must know when that is another stream."""
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None and t.is_cuda:
-        t.record_stream(stream)
+    one).  It belongs to the stream that writes it: memory of the current
+    stream may still be in use there by calls that another stream does not
+    wait for.  The current stream, on which the caller goes on, is made known
+    to the allocator."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream) or stream.device != device:
+        raise ValueError(f"stream must be a torch.cuda.Stream of {device} (got {stream!r})")
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if current != stream:
+        t.record_stream(current)
     return t
 
 
