@@ -422,7 +422,10 @@ typedef struct {
 /* Norm and rotation of all query and key heads in one pass: q_out and k_out
  * (bf16, rounded to nearest even) from q and k, tokens rows each.
  * positions: device int32 [tokens].  k (and k_out) may be null.  An output
- * may be its input (same data and strides); other overlaps are not allowed. */
+ * may be its input (same data and strides); any other overlap of an output
+ * with an input or the other output is NVFP4_ERR_INVALID_ARG.  Rows of one
+ * token stride may lie between one another's; with two token strides, memory
+ * from the first row to the last counts as the tensor's. */
 int nvfp4_qk_norm_rope(const nvfp4_heads *q, const nvfp4_heads *k, const nvfp4_heads *q_out, const nvfp4_heads *k_out,
                        int64_t tokens, int64_t head_dim, const int32_t *positions, const nvfp4_norm_rope *norm_rope,
                        void *stream);
@@ -455,8 +458,10 @@ size_t nvfp4_fp8_kv_attention_workspace_bytes(int64_t tokens, int64_t q_heads, i
  * to bf16.  A token that sees no key gets zeros.  Keys out of sight never
  * influence a token, whatever bytes they hold.  out_amax, if not null,
  * receives max|out| over the rows written (bf16 magnitude bits, the form
- * NVFP4_AMAX_GIVEN takes).  out must not overlap q or gate.  q_heads is a
- * multiple of kv_heads, at most 128 times it.
+ * NVFP4_AMAX_GIVEN takes).  out must not overlap q or gate, nor ws any of
+ * them or out_amax (NVFP4_ERR_INVALID_ARG; what counts as an overlap:
+ * nvfp4_qk_norm_rope).  q_heads is a multiple of kv_heads, at most 128 times
+ * it.
  * Softmax statistics and sums are fp32.  In tiles of several tokens queries
  * enter the FP8 MMA as the sum of two E4M3 terms, which hold all 8 bits of a
  * bf16 value (values below 2^-10 of their row's largest lose low bits),

@@ -5,6 +5,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -47,6 +48,75 @@ int check_heads(const nvfp4_heads *x, int64_t tokens)
     if (!aligned(x->data, 16) || x->token_stride % 8 != 0 || x->head_stride % 8 != 0)
         return NVFP4_ERR_MISALIGNED;
     return NVFP4_OK;
+}
+
+// Bytes [lo, hi) that head rows span, gaps between them included.
+struct Span {
+    __int128 lo, hi;
+    bool meets(const Span &o) const { return lo < o.hi && o.lo < hi; }
+};
+
+Span span_of(const void *p, __int128 bytes)
+{
+    const __int128 lo = static_cast<__int128>(reinterpret_cast<uintptr_t>(p));
+    return {lo, lo + bytes};
+}
+
+Span span_of(const nvfp4_heads &x, int64_t tokens, int64_t head_dim)
+{
+    Span s = span_of(x.data, 2 * head_dim);
+    for (const __int128 reach : {static_cast<__int128>(tokens - 1) * x.token_stride, static_cast<__int128>(x.heads - 1) * x.head_stride})
+        (reach < 0 ? s.lo : s.hi) += 2 * reach;
+    return s;
+}
+
+bool same_rows(const nvfp4_heads &a, const nvfp4_heads &b, int64_t tokens)
+{
+    return a.data == b.data && a.heads == b.heads && (tokens == 1 || a.token_stride == b.token_stride) &&
+           (a.heads == 1 || a.head_stride == b.head_stride);
+}
+
+// Whether some row of `a` and some row of `b` share an element.  Views of one
+// projection's output have one token stride: there the answer is exact.  With
+// two token strides, spans that meet count as an overlap.
+bool rows_meet(const nvfp4_heads &a, const nvfp4_heads &b, int64_t tokens, int64_t head_dim)
+{
+    const Span sa = span_of(a, tokens, head_dim), sb = span_of(b, tokens, head_dim);
+    if (!sa.meets(sb))
+        return false;
+    if (tokens > 1 && a.token_stride != b.token_stride)
+        return true;
+    constexpr int64_t kFar = int64_t(1) << 50;  // beyond any memory, and the sums below stay in 64 bits
+    if (sa.hi - sa.lo > kFar || sb.hi - sb.lo > kFar)
+        return true;
+    const int64_t step = tokens > 1 ? std::abs(a.token_stride) : 0;
+    const int64_t apart = (static_cast<const char *>(b.data) - static_cast<const char *>(a.data)) / 2;
+    const int64_t ha = a.heads > 1 ? a.head_stride : 0, hb = b.heads > 1 ? b.head_stride : 0;
+    // rows of one token next to those of the other within a token's stride: columns of one projection's output
+    const int64_t wide_a = (a.heads - 1) * ha + head_dim, wide_b = (b.heads - 1) * hb + head_dim;
+    if (step > 0 && ha >= 0 && hb >= 0) {
+        const int64_t at = ((apart % step) + step) % step;
+        if (wide_a <= at && at + wide_b <= step)
+            return false;
+    }
+    // a row of b that lies `d` elements behind one of a, at the same token or at tokens - 1 others at most
+    auto near = [&](int64_t d) {
+        if (step == 0)
+            return std::abs(d) < head_dim;
+        const int64_t n = std::min<int64_t>(std::abs(d) / step, tokens - 1), rest = std::abs(d) - n * step;
+        return rest < head_dim || (n + 1 < tokens && step - rest < head_dim);
+    };
+    if (ha == hb) {  // only the difference of two heads counts
+        for (int64_t h = 1 - a.heads; h < b.heads; ++h)
+            if (near(apart + h * ha))
+                return true;
+        return false;
+    }
+    for (int64_t i = 0; i < a.heads; ++i)
+        for (int64_t k = 0; k < b.heads; ++k)
+            if (near(apart + k * hb - i * ha))
+                return true;
+    return false;
 }
 
 int check_tokens(int64_t tokens)
@@ -300,6 +370,12 @@ extern "C" int nvfp4_qk_norm_rope(const nvfp4_heads *q, const nvfp4_heads *k, co
         return NVFP4_ERR_MISALIGNED;
     if (tokens == 0)
         return NVFP4_OK;
+    // warps read rows while others write theirs; a row that is its own output is read before it is written
+    if ((!same_rows(*q, *q_out, tokens) && rows_meet(*q, *q_out, tokens, head_dim)) ||
+        (k != nullptr && ((!same_rows(*k, *k_out, tokens) && rows_meet(*k, *k_out, tokens, head_dim)) ||
+                          rows_meet(*q_out, *k_out, tokens, head_dim) || rows_meet(*q, *k_out, tokens, head_dim) ||
+                          rows_meet(*k, *q_out, tokens, head_dim))))
+        return NVFP4_ERR_INVALID_ARG;
     nvfp4::host::Device d;
     rc = nvfp4::host::device(&d);
     if (rc != NVFP4_OK)
@@ -423,6 +499,15 @@ extern "C" int nvfp4_fp8_kv_attention(const nvfp4_heads *q, const nvfp4_heads *g
     if (ws == nullptr ||
         ws_bytes < nvfp4_fp8_kv_attention_workspace_bytes(tokens, q->heads, cache->kv_heads, cache->head_dim))
         return NVFP4_ERR_WORKSPACE;
+    const int64_t dim = cache->head_dim;
+    const Span scratch = span_of(ws, nvfp4_fp8_kv_attention_workspace_bytes(tokens, q->heads, cache->kv_heads, dim));
+    if (out_amax != nullptr && scratch.meets(span_of(out_amax, 4)))
+        return NVFP4_ERR_INVALID_ARG;
+    // CTAs read an item's queries and gates while others write their results
+    if (tokens > 0 && (rows_meet(*q, *out, tokens, dim) || (gate != nullptr && rows_meet(*gate, *out, tokens, dim)) ||
+                       scratch.meets(span_of(*out, tokens, dim)) || scratch.meets(span_of(*q, tokens, dim)) ||
+                       (gate != nullptr && scratch.meets(span_of(*gate, tokens, dim)))))
+        return NVFP4_ERR_INVALID_ARG;
     nvfp4::host::Device d;
     rc = nvfp4::host::device(&d);
     if (rc != NVFP4_OK)
