@@ -443,8 +443,14 @@ int nvfp4_fp8_kv_append(const nvfp4_heads *k, const nvfp4_heads *v, int64_t toke
 
 typedef struct {
     float softmax_scale; /* positive, finite */
-    unsigned flags;      /* 0 */
+    unsigned flags;      /* 0 or NVFP4_SINGLE_TOKENS */
 } nvfp4_attention_opts;
+
+/* nvfp4_attention_opts.flags: the caller expects no sequence to have more than
+ * one new token (a decode step).  The kernel for longer ones is left out, 2 to
+ * 5 us less; should there be longer ones all the same, results are as right,
+ * and slow. */
+#define NVFP4_SINGLE_TOKENS 16u
 
 /* Workspace bytes of nvfp4_fp8_kv_attention (0 for invalid sizes). */
 size_t nvfp4_fp8_kv_attention_workspace_bytes(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t head_dim);

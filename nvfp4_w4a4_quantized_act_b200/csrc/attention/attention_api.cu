@@ -489,7 +489,7 @@ extern "C" int nvfp4_fp8_kv_attention(const nvfp4_heads *q, const nvfp4_heads *g
         rc = check_heads(gate, tokens);
     if (rc != NVFP4_OK)
         return rc;
-    if (opts == nullptr || opts->flags != 0 || !(opts->softmax_scale > 0.0f) || !std::isfinite(opts->softmax_scale) ||
+    if (opts == nullptr || (opts->flags & ~NVFP4_SINGLE_TOKENS) != 0 || !(opts->softmax_scale > 0.0f) || !std::isfinite(opts->softmax_scale) ||
         out->heads != q->heads || (gate != nullptr && gate->heads != q->heads))
         return NVFP4_ERR_INVALID_ARG;
     if (q->heads % cache->kv_heads != 0 || q->heads / cache->kv_heads > 128)
@@ -522,17 +522,21 @@ extern "C" int nvfp4_fp8_kv_attention(const nvfp4_heads *q, const nvfp4_heads *g
         return NVFP4_OK;
     // Sequences with one new token go to the kernel for single tokens where the
     // heads that share a key fit its rows.  The lengths are on the device, so
-    // the sizes have to say which kernels may find work.  As many token rows as
-    // sequences: single tokens, padded or not, and all go there (it is right
-    // for longer ones too, but reads their keys again for every token).  Fewer
-    // rows, or a few more, may be single tokens or a chunk among sequences that
-    // stand still, and many sequences hold both kinds: both kernels, of which
-    // the tile kernel costs some 2 us when it finds nothing.  Else the tile
-    // kernel takes everything.
+    // the sizes have to say which kernels may find work.  One row alone is a
+    // single token.  As many rows as sequences, fewer or a few more may be
+    // single tokens, padded or not, or a chunk among sequences that stand
+    // still, and many sequences hold both kinds: both kernels.  Else the tile
+    // kernel takes everything.  Where the caller expects single tokens, their
+    // kernel takes everything: it is right for more tokens too, but reads their
+    // keys again for each.  Measured (us, both kernels against that one alone):
+    // 2 x 777 keys of 4 heads of 256: 13.4 against 11.5; 64 x 500: 24.4 against
+    // 21.1; 64 x 8192: 117.8 against 113.3; a chunk of 64 tokens at 8192 beside
+    // 63 sequences that stand still: 44.8 against 138.8.
     const int64_t group = q->heads / cache->kv_heads;
+    const bool expected = (opts->flags & NVFP4_SINGLE_TOKENS) != 0;
     const bool single = group <= attn::DECODE_ROWS &&
-                        (int64_t(batch->num_seqs) * cache->kv_heads >= kMixedItems || tokens <= int64_t(batch->num_seqs) + kPadRows);
-    const bool tiled = !single || tokens != batch->num_seqs;
+                        (expected || int64_t(batch->num_seqs) * cache->kv_heads >= kMixedItems || tokens <= int64_t(batch->num_seqs) + kPadRows);
+    const bool tiled = !single || (tokens > 1 && !expected);
     attn::AttnParams p;
     p.q = rows_of(q);
     p.gate = rows_of(gate);

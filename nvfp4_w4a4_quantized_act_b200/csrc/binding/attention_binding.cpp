@@ -312,10 +312,10 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n)
     });
 }
 
-// q, k_pages, v_pages, k_scale, v_scale, page_table, cu_tokens, seq_lens, softmax_scale, gate, out, out_amax, ws, stream
+// q, k_pages, v_pages, k_scale, v_scale, page_table, cu_tokens, seq_lens, softmax_scale, gate, out, out_amax, ws, single_tokens, stream
 PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
-    return guarded("fp8_kv_attention", n, 14, [&] {
+    return guarded("fp8_kv_attention", n, 15, [&] {
         Call c;
         const at::Tensor &q = *tensor(a[0], "q"), &out = *tensor(a[10], "out"), &ws = *tensor(a[12], "ws");
         const at::Tensor *gate = tensor(a[9], "gate", true), *amax = tensor(a[11], "out_amax", true);
@@ -343,8 +343,9 @@ PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t n)
             c.on(*amax, "out_amax");
         }
         const nvfp4_attention_opts opts{
-            static_cast<float>(a[8] == Py_None ? 1.0 / std::sqrt(static_cast<double>(q.size(2))) : number(a[8], "softmax_scale")), 0};
-        void *stream = c.stream(a[13]);
+            static_cast<float>(a[8] == Py_None ? 1.0 / std::sqrt(static_cast<double>(q.size(2))) : number(a[8], "softmax_scale")),
+            PyObject_IsTrue(a[13]) == 1 ? NVFP4_SINGLE_TOKENS : 0u};
+        void *stream = c.stream(a[14]);
         return without_gil([&] {
             return g.attend(&hq, gate != nullptr ? &hg : nullptr, &ho, q.size(0), &pages, &batch, &opts,
                             amax != nullptr ? static_cast<uint32_t *>(amax->data_ptr()) : nullptr, ws.data_ptr(), ws.nbytes(), stream);

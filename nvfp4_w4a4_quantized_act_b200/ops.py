@@ -588,12 +588,15 @@ def fp8_kv_attention_workspace_bytes(tokens: int, q_heads: int, kv_heads: int, h
 
 
 def fp8_kv_attention(q, k_pages, v_pages, k_scale, v_scale, page_table, cu_tokens, seq_lens, softmax_scale=None,
-                     gate=None, out=None, out_amax=None, ws=None, stream=None):
+                     gate=None, out=None, out_amax=None, ws=None, single_tokens=False, stream=None):
     """nvfp4_fp8_kv_attention -> out: causal attention of the batch's new
     tokens, q bf16 [tokens, q_heads, head_dim], over their sequences' pages,
     times sigmoid(gate); out must not overlap q or gate.  softmax_scale defaults
     to head_dim ** -0.5; out_amax (4 bytes, e.g. the first word of a quantize
-    workspace) receives max|out| for quantize_act(..., amax_given=True)."""
+    workspace) receives max|out| for quantize_act(..., amax_given=True).
+    single_tokens: no sequence is expected to have more than one new token (a
+    decode step), which leaves out the kernel for longer ones; a wrong guess is
+    slow, not wrong."""
     if out is None:
         out = _new(stream, q.shape, torch.bfloat16, q.device)
     if ws is None:
@@ -601,7 +604,7 @@ def fp8_kv_attention(q, k_pages, v_pages, k_scale, v_scale, page_table, cu_token
             if q.dim() == 3 and k_pages.dim() == 4 else 0
         ws = _new(stream, max(need, 16), torch.uint8, q.device)
     rc = (_native or _attention()).fp8_kv_attention(q, k_pages, v_pages, k_scale, v_scale, page_table, cu_tokens, seq_lens,
-                                                    softmax_scale, gate, out, out_amax, ws, stream)
+                                                    softmax_scale, gate, out, out_amax, ws, single_tokens, stream)
     if rc:
         raise Nvfp4Error(rc, "nvfp4_fp8_kv_attention")
     return out

@@ -23,3 +23,16 @@ def test_short_prompts_with_queries_of_different_size(D, kv, n):
         out = ops.fp8_kv_attention(q, *c.args())
         assert ops.get_status() == 0
     check_attention(c, q, None, out, D ** -0.5, only=set(range(0, 150, 10)) | {149})
+
+
+@pytest.mark.parametrize("single", [False, True])
+@pytest.mark.parametrize("seqs", [[(64, 900)] + [(0, 70)] * 63, [(1, 900), (1, 0), (1, 129)], [(1, 300)], [(3, 130), (0, 5), (40, 700), (1, 64)]])
+@pytest.mark.parametrize("D,heads", [(128, 4), (256, 12), (256, 40)])
+def test_one_token_expected_or_not(D, heads, seqs, single):
+    """A promise of single tokens changes which kernel runs, not what is right."""
+    c = Cache(seqs, 2, D, 32, seed=heads)
+    fill_normal(c, 4)
+    q, gate = (torch.randn(c.tokens, heads, D, generator=gen(i), device=DEV).to(torch.bfloat16) for i in (1, 2))
+    out = ops.fp8_kv_attention(q, *c.args(), gate=gate, single_tokens=single)
+    assert ops.get_status() == 0
+    check_attention(c, q, gate, out, D ** -0.5)

@@ -32,7 +32,7 @@ def fake(tmp_path_factory):
     return L
 
 
-def attend(L, tokens, seqs, heads=24, kv=4, dim=256, refuse=-1, q=None, gate=None, out=None, amax=None, ws=FAKE + (2 << 40)):
+def attend(L, tokens, seqs, heads=24, kv=4, dim=256, refuse=-1, q=None, gate=None, out=None, amax=None, ws=FAKE + (2 << 40), flags=0):
     """(status, kernels launched, in order)."""
     L.fake_reset(refuse)
     page = 16
@@ -42,7 +42,7 @@ def attend(L, tokens, seqs, heads=24, kv=4, dim=256, refuse=-1, q=None, gate=Non
                     v_page_stride=page * kv * dim, v_token_stride=kv * dim, v_head_stride=dim)
     batch = KvBatch(FAKE, FAKE, FAKE, 64, seqs, 64)
     rc = L.nvfp4_fp8_kv_attention(ctypes.byref(q), ctypes.byref(gate) if gate else None, ctypes.byref(o), tokens, ctypes.byref(pages),
-                                  ctypes.byref(batch), ctypes.byref(AttentionOpts(0.1, 0)), amax, ws,
+                                  ctypes.byref(batch), ctypes.byref(AttentionOpts(0.1, flags)), amax, ws,
                                   L.nvfp4_fp8_kv_attention_workspace_bytes(tokens, heads, kv, dim), None)
     kinds = {"join": "join", "paged_attention_kernel": "tiles", "paged_decode_kernel": "single"}
     names = [L.fake_name(i).decode() for i in range(L.fake_launches())]
@@ -135,3 +135,25 @@ def test_a_workspace_that_is_something_else(fake):
     for which in ("q", "gate", "out"):
         assert attend(fake, 40, 1, **{which: Heads(ws - 16, 24 * 256, 256, 24)}) == (1, [])
         assert attend(fake, 40, 1, **{which: Heads(ws + size, 24 * 256, 256, 24)})[0] == 0
+
+
+@pytest.mark.parametrize("tokens,seqs,heads,flags,want", [
+    (64, 64, 24, 0, "tiles single join"),   # single tokens, or a chunk of 64 among sequences that stand still
+    (2, 2, 24, 0, "tiles single join"),
+    (67, 64, 24, 0, "tiles single join"),
+    (20, 64, 24, 0, "tiles single join"),
+    (4000, 93, 24, 0, "tiles single join"),
+    (73, 64, 24, 0, "tiles join"),
+    (1, 1, 24, 0, "single join"),           # nothing but a single token can be
+    (1, 40, 24, 0, "single join"),
+    (64, 64, 24, 16, "single join"),        # the caller's word
+    (300, 64, 24, 16, "single join"),
+    (64, 64, 36, 16, "tiles join"),         # more heads share a key than that kernel has rows
+    (64, 64, 36, 0, "tiles join"),
+])
+def test_which_kernels_run(fake, tokens, seqs, heads, flags, want):
+    assert attend(fake, tokens, seqs, heads=heads, flags=flags) == (0, want.split())
+
+
+def test_other_flags_are_refused(fake):
+    assert attend(fake, 4, 4, flags=8) == (1, []) and attend(fake, 4, 4, flags=17) == (1, [])
