@@ -232,6 +232,16 @@ double number(PyObject *o, const char *name)
     return v;
 }
 
+bool truth(PyObject *o, const char *name)
+{
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) {
+        PyErr_Clear();
+        throw Refused(std::string(name) + " must be true or false");
+    }
+    return v != 0;
+}
+
 // Runs a call with C++ exceptions turned into Python's.
 template <typename F>
 PyObject *guarded(const char *name, Py_ssize_t got, Py_ssize_t want, F f)
@@ -281,7 +291,7 @@ PyObject *norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n)
         if (inv_freq != nullptr && positions == nullptr)
             throw Refused("a rotation needs positions");
         const nvfp4_norm_rope nr = c.norm_rope(q.size(2), inv_freq, tensor(a[4], "q_weight", true),
-                                               tensor(a[5], "k_weight", true), number(a[6], "eps"), PyObject_IsTrue(a[7]) == 1);
+                                               tensor(a[5], "k_weight", true), number(a[6], "eps"), truth(a[7], "plus_one"));
         const auto *pos = static_cast<const int32_t *>(c.vector(positions, "positions", at::kInt, q.size(0)));
         void *stream = c.stream(a[10]);
         return without_gil([&] {
@@ -304,7 +314,7 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n)
             refuse("k", "has other heads or another head_dim than the pages", k);
         const nvfp4_kv_batch batch = c.batch(*tensor(a[6], "page_table"), *tensor(a[7], "cu_tokens"), *tensor(a[8], "seq_lens"));
         const nvfp4_norm_rope nr = c.norm_rope(k.size(2), tensor(a[9], "inv_freq", true), nullptr,
-                                               tensor(a[10], "k_weight", true), number(a[11], "eps"), PyObject_IsTrue(a[12]) == 1);
+                                               tensor(a[10], "k_weight", true), number(a[11], "eps"), truth(a[12], "plus_one"));
         const auto *pos =
             static_cast<const int32_t *>(c.vector(tensor(a[13], "positions", true), "positions", at::kInt, k.size(0)));
         void *stream = c.stream(a[14]);
@@ -344,7 +354,7 @@ PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t n)
         }
         const nvfp4_attention_opts opts{
             static_cast<float>(a[8] == Py_None ? 1.0 / std::sqrt(static_cast<double>(q.size(2))) : number(a[8], "softmax_scale")),
-            PyObject_IsTrue(a[13]) == 1 ? NVFP4_SINGLE_TOKENS : 0u};
+            truth(a[13], "single_tokens") ? NVFP4_SINGLE_TOKENS : 0u};
         void *stream = c.stream(a[14]);
         return without_gil([&] {
             return g.attend(&hq, gate != nullptr ? &hg : nullptr, &ho, q.size(0), &pages, &batch, &opts,
