@@ -183,8 +183,8 @@ int check_batch(const nvfp4_kv_batch *b, int32_t page_size)
     if (b->num_seqs > 0 && (b->cu_tokens == nullptr || b->seq_lens == nullptr ||
                             (b->max_pages > 0 && b->page_table == nullptr) || b->table_stride < b->max_pages))
         return NVFP4_ERR_INVALID_ARG;
-    // positions are 32-bit
-    if (b->num_seqs > (1 << 20) || int64_t(b->max_pages) * page_size >= (int64_t(1) << 31))
+    // positions are 32-bit, and so are they rounded up to the end of a key block and the block behind it
+    if (b->num_seqs > (1 << 20) || int64_t(b->max_pages) * page_size > (int64_t(1) << 31) - 2 * attn::KEY_BLOCK)
         return NVFP4_ERR_UNSUPPORTED_SHAPE;
     if (!aligned(b->cu_tokens, 4) || !aligned(b->seq_lens, 4) || !aligned(b->page_table, 4))
         return NVFP4_ERR_MISALIGNED;
@@ -493,6 +493,12 @@ extern "C" int nvfp4_fp8_kv_attention(const nvfp4_heads *q, const nvfp4_heads *g
         out->heads != q->heads || (gate != nullptr && gate->heads != q->heads))
         return NVFP4_ERR_INVALID_ARG;
     if (q->heads % cache->kv_heads != 0 || q->heads / cache->kv_heads > 128)
+        return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    // The line of cost, times the number of CTAs, stays in 64 bits whatever the offsets and lengths hold: an item for
+    // every sequence, row and key head, each with the longest length.
+    const double line = double(batch->num_seqs) * double(tokens) * cache->kv_heads *
+                        (double(batch->max_pages) * cache->page_size + attn::ROW_TILE + kTileItemCost256);
+    if (line * attn::CTAS > 9e18)
         return NVFP4_ERR_UNSUPPORTED_SHAPE;
     if (!aligned(out_amax, 4) || !aligned(ws, 16))
         return NVFP4_ERR_MISALIGNED;

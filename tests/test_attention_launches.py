@@ -32,7 +32,8 @@ def fake(tmp_path_factory):
     return L
 
 
-def attend(L, tokens, seqs, heads=24, kv=4, dim=256, refuse=-1, q=None, gate=None, out=None, amax=None, ws=FAKE + (2 << 40), flags=0):
+def attend(L, tokens, seqs, heads=24, kv=4, dim=256, refuse=-1, q=None, gate=None, out=None, amax=None, ws=FAKE + (2 << 40), flags=0,
+           max_pages=64):
     """(status, kernels launched, in order)."""
     L.fake_reset(refuse)
     page = 16
@@ -40,7 +41,7 @@ def attend(L, tokens, seqs, heads=24, kv=4, dim=256, refuse=-1, q=None, gate=Non
     pages = KvPages(k_pages=FAKE, v_pages=FAKE, k_scale=FAKE, v_scale=FAKE, num_pages=64, page_size=page, kv_heads=kv, head_dim=dim,
                     k_page_stride=page * kv * dim, k_token_stride=kv * dim, k_head_stride=dim,
                     v_page_stride=page * kv * dim, v_token_stride=kv * dim, v_head_stride=dim)
-    batch = KvBatch(FAKE, FAKE, FAKE, 64, seqs, 64)
+    batch = KvBatch(FAKE, FAKE, FAKE, max_pages, seqs, max_pages)
     rc = L.nvfp4_fp8_kv_attention(ctypes.byref(q), ctypes.byref(gate) if gate else None, ctypes.byref(o), tokens, ctypes.byref(pages),
                                   ctypes.byref(batch), ctypes.byref(AttentionOpts(0.1, flags)), amax, ws,
                                   L.nvfp4_fp8_kv_attention_workspace_bytes(tokens, heads, kv, dim), None)
@@ -157,3 +158,14 @@ def test_which_kernels_run(fake, tokens, seqs, heads, flags, want):
 
 def test_other_flags_are_refused(fake):
     assert attend(fake, 4, 4, flags=8) == (1, []) and attend(fake, 4, 4, flags=17) == (1, [])
+
+
+def test_sizes_whose_sums_leave_the_integers(fake):
+    """A position rounded up to the end of a key block, and the block behind it,
+    fit 32 bits; the cost of a batch, times the number of CTAs, fits 64 bits
+    even if every sequence claimed every row and the longest length."""
+    most = (2 ** 31 - 256) // 16
+    assert attend(fake, 4, 2, max_pages=most)[0] == 0
+    assert attend(fake, 4, 2, max_pages=most + 1) == (2, [])
+    assert attend(fake, 1 << 16, 1 << 12, max_pages=1 << 16)[0] == 0      # 4096 sequences, 2^20 keys each
+    assert attend(fake, 1 << 20, 1 << 20, max_pages=1 << 24) == (2, [])
