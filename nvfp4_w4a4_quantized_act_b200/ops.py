@@ -14,6 +14,8 @@ from dataclasses import dataclass
 
 import torch
 
+from .build import binding_path
+
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libnvfp4.so")
 
@@ -513,7 +515,7 @@ def fp8_kv_quantize(X: torch.Tensor, scale: torch.Tensor, out=None, stream=None)
 # a CPython module (csrc/binding), which raises ValueError where the other
 # calls' checks here do.
 
-BINDING_PATH = os.path.join(_PKG, "_attention.so")
+BINDING_PATH = binding_path(torch.__version__)
 _native = None
 
 
