@@ -201,8 +201,31 @@ def act_scale_offset() -> int:
     return int(lib().nvfp4_linear_act_scale_offset())
 
 
-def _empty_u8(n, device):
-    return torch.empty(max(int(n), 1), dtype=torch.uint8, device=device)
+def _new(stream, shape, dtype, device):
+    """An output or scratch tensor for a call on `stream` (None: the current
+    one).  It belongs to the stream that writes it: memory of the current
+    stream may still be in use there by calls that another stream does not
+    wait for.  The current stream, on which the caller goes on, is made known
+    to the allocator."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        if not isinstance(getattr(stream, "cuda_stream", None), int):
+            raise ValueError(f"stream must be a torch.cuda.Stream (got {stream!r})")
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+    current = torch.cuda.current_stream(device)
+    if stream == current:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)
+    return t
+
+
+def _empty_u8(n, device, stream=None):
+    return _new(stream, max(int(n), 1), torch.uint8, device)
 
 
 @dataclass
@@ -225,10 +248,10 @@ def quantize_weights(W: torch.Tensor, segments=None, stream=None) -> QuantizedWe
     N, K = W.shape
     segments = [(0, N)] if segments is None else [(int(a), int(b)) for a, b in segments]
     dev = W.device
-    codes = _empty_u8(N * K // 2, dev)
-    sf = _empty_u8(sf_bytes(N, K), dev)
-    g_w = torch.empty(len(segments), dtype=torch.float32, device=dev)
-    ws = _empty_u8(quant_workspace_bytes(len(segments)), dev)
+    codes = _empty_u8(N * K // 2, dev, stream)
+    sf = _empty_u8(sf_bytes(N, K), dev, stream)
+    g_w = _new(stream, len(segments), torch.float32, dev)
+    ws = _empty_u8(quant_workspace_bytes(len(segments)), dev, stream)
     arr, n = _segs(segments)
     _check(lib().nvfp4_quantize_weights(_p(W), N, K, W.stride(0), arr, n, _p(codes), _p(sf), _p(g_w), _p(ws),
                                         _nbytes(ws), _stream(stream)), "nvfp4_quantize_weights")
@@ -243,18 +266,18 @@ def quantize_act(X: torch.Tensor, g_a: torch.Tensor | None = None, static_scale:
     M, K = X.shape
     dev = X.device
     if codes is None:
-        codes = _empty_u8(M * K // 2, dev)
+        codes = _empty_u8(M * K // 2, dev, stream)
     _buffer(codes, M * K // 2, "codes")
     if sf is None:
-        sf = _empty_u8(sf_bytes(M, K), dev)
+        sf = _empty_u8(sf_bytes(M, K), dev, stream)
     _buffer(sf, sf_bytes(M, K), "sf")
     if g_a is None:
         if static_scale:
             raise ValueError("static_scale needs the calibrated scale g_a")
-        g_a = torch.empty(1, dtype=torch.float32, device=dev)
+        g_a = _new(stream, 1, torch.float32, dev)
     _buffer(g_a, 4, "g_a", torch.float32)
     if ws is None:
-        ws = _empty_u8(quant_workspace_bytes(1), dev)
+        ws = _empty_u8(quant_workspace_bytes(1), dev, stream)
     _buffer(ws, 0, "ws")
     flags = (NVFP4_STATIC_SCALE if static_scale else 0) | (NVFP4_AMAX_GIVEN if amax_given else 0)
     _check(lib().nvfp4_quantize_act(_p(X), M, K, X.stride(0), _p(codes), _p(sf), _p(g_a), flags, _p(ws),
@@ -278,7 +301,7 @@ def gemm_prequant(a_codes, a_sf, g_a, M: int, K: int, w: QuantizedWeight, out=No
     _buffer(g_a, 4, "g_a", torch.float32)
     dt = torch.float32 if out_fp32 else torch.bfloat16
     if out is None:
-        out = torch.empty((M, w.N), dtype=dt, device=a_codes.device)
+        out = _new(stream, (M, w.N), dt, a_codes.device)
     _buffer(out, M * w.N * out.element_size(), "out", dt)
     arr, n = _segs(w.segments)
     flags = (NVFP4_OUT_FP32 if out_fp32 else 0) | debug_flags
@@ -303,10 +326,10 @@ def linear_fused(X: torch.Tensor, w: QuantizedWeight, out=None, out_fp32=False, 
     _same_k(K, w)
     dt = torch.float32 if out_fp32 else torch.bfloat16
     if out is None:
-        out = torch.empty((M, w.N), dtype=dt, device=X.device)
+        out = _new(stream, (M, w.N), dt, X.device)
     _buffer(out, M * w.N * out.element_size(), "out", dt)
     if ws is None:
-        ws = _empty_u8(workspace_bytes(M, w.N, K, len(w.segments)), X.device)
+        ws = _empty_u8(workspace_bytes(M, w.N, K, len(w.segments)), X.device, stream)
     _buffer(ws, 0, "ws")
     arr, n = _segs(w.segments)
     flags = (NVFP4_OUT_FP32 if out_fp32 else 0) | (NVFP4_STATIC_SCALE if static_scale else 0)
@@ -324,10 +347,10 @@ def linear(X: torch.Tensor, w: QuantizedWeight, out=None, out_fp32=False, ws=Non
     _same_k(K, w)
     dt = torch.float32 if out_fp32 else torch.bfloat16
     if out is None:
-        out = torch.empty((M, w.N), dtype=dt, device=X.device)
+        out = _new(stream, (M, w.N), dt, X.device)
     _buffer(out, M * w.N * out.element_size(), "out", dt)
     if ws is None:
-        ws = _empty_u8(workspace_bytes(M, w.N, K, 1), X.device)
+        ws = _empty_u8(workspace_bytes(M, w.N, K, 1), X.device, stream)
     _buffer(ws, 0, "ws")
     flags = NVFP4_OUT_FP32 if out_fp32 else 0
     _check(lib().nvfp4_linear(_p(X), M, K, _p(w.codes), _p(w.sf), _p(w.g_w), w.N, _p(out), flags, _p(ws),
@@ -356,19 +379,19 @@ def swiglu_quantize(gate_up: torch.Tensor, h=None, codes=None, sf=None, g_h=None
     F = F2 // 2
     dev = gate_up.device
     if h is None:
-        h = torch.empty((M, F), dtype=torch.bfloat16, device=dev)
+        h = _new(stream, (M, F), torch.bfloat16, dev)
     _buffer(h, M * F * 2, "h", torch.bfloat16)
     if codes is None:
-        codes = _empty_u8(M * F // 2, dev)
+        codes = _empty_u8(M * F // 2, dev, stream)
     _buffer(codes, M * F // 2, "codes")
     if sf is None:
-        sf = _empty_u8(sf_bytes(M, F), dev)
+        sf = _empty_u8(sf_bytes(M, F), dev, stream)
     _buffer(sf, sf_bytes(M, F), "sf")
     if g_h is None:
-        g_h = torch.empty(1, dtype=torch.float32, device=dev)
+        g_h = _new(stream, 1, torch.float32, dev)
     _buffer(g_h, 4, "g_h", torch.float32)
     if ws is None:
-        ws = _empty_u8(quant_workspace_bytes(1), dev)
+        ws = _empty_u8(quant_workspace_bytes(1), dev, stream)
     _buffer(ws, 0, "ws")
     _check(lib().nvfp4_swiglu_quantize(_p(gate_up), M, F, gate_up.stride(0), _p(h), _p(codes), _p(sf), _p(g_h),
                                        _p(ws), _nbytes(ws), _stream(stream)), "nvfp4_swiglu_quantize")
@@ -390,7 +413,7 @@ def linear_fused_noalloc(X: torch.Tensor, w: QuantizedWeight, out=None, out_fp32
     _same_k(K, w)
     dt = torch.float32 if out_fp32 else torch.bfloat16
     if out is None:
-        out = torch.empty((M, w.N), dtype=dt, device=X.device)
+        out = _new(stream, (M, w.N), dt, X.device)
     _buffer(out, M * w.N * out.element_size(), "out", dt)
     arr, n = _segs(w.segments)
     flags = NVFP4_OUT_FP32 if out_fp32 else 0
@@ -409,10 +432,10 @@ def quantize_weights_gated(W: torch.Tensor, stream=None) -> QuantizedWeight:
     N, K = W.shape
     F = N // 2
     dev = W.device
-    codes = _empty_u8(N * K // 2, dev)
-    sf = _empty_u8(sf_bytes(N, K), dev)
-    g_w = torch.empty(2, dtype=torch.float32, device=dev)
-    ws = _empty_u8(quant_workspace_bytes(2), dev)
+    codes = _empty_u8(N * K // 2, dev, stream)
+    sf = _empty_u8(sf_bytes(N, K), dev, stream)
+    g_w = _new(stream, 2, torch.float32, dev)
+    ws = _empty_u8(quant_workspace_bytes(2), dev, stream)
     _check(lib().nvfp4_quantize_weights_gated(_p(W), F, K, W.stride(0), _p(codes), _p(sf), _p(g_w), _p(ws),
                                               _nbytes(ws), _stream(stream)), "nvfp4_quantize_weights_gated")
     return QuantizedWeight(codes[: N * K // 2].view(N, K // 2), sf, g_w, [(0, F), (F, N)], N, K, gated=True)
@@ -429,19 +452,19 @@ def linear_swiglu(X: torch.Tensor, w: QuantizedWeight, h=None, h_codes=None, h_s
     F = w.N // 2
     dev = X.device
     if h is None:
-        h = torch.empty((M, F), dtype=torch.bfloat16, device=dev)
+        h = _new(stream, (M, F), torch.bfloat16, dev)
     _buffer(h, M * F * 2, "h", torch.bfloat16)
     if h_codes is None:
-        h_codes = _empty_u8(M * F // 2, dev)
+        h_codes = _empty_u8(M * F // 2, dev, stream)
     _buffer(h_codes, M * F // 2, "h_codes")
     if h_sf is None:
-        h_sf = _empty_u8(sf_bytes(M, F), dev)
+        h_sf = _empty_u8(sf_bytes(M, F), dev, stream)
     _buffer(h_sf, sf_bytes(M, F), "h_sf")
     if g_h is None:
-        g_h = torch.empty(1, dtype=torch.float32, device=dev)
+        g_h = _new(stream, 1, torch.float32, dev)
     _buffer(g_h, 4, "g_h", torch.float32)
     if ws is None:
-        ws = _empty_u8(workspace_bytes(M, w.N, K, 2), dev)
+        ws = _empty_u8(workspace_bytes(M, w.N, K, 2), dev, stream)
     _buffer(ws, 0, "ws")
     flags = (NVFP4_STATIC_SCALE if static_scale else 0) | (NVFP4_SINGLE_CTA if single_cta else 0)
     _check(lib().nvfp4_linear_swiglu(_p(X), M, K, _p(w.codes), _p(w.sf), F, _p(w.g_w), _p(h), _p(h_codes),
@@ -460,10 +483,10 @@ def gemm_prequant_swiglu(a_codes, a_sf, g_a, M: int, K: int, w: QuantizedWeight,
     _buffer(g_a, 4, "g_a", torch.float32)
     F = w.N // 2
     if h is None:
-        h = torch.empty((M, F), dtype=torch.bfloat16, device=a_codes.device)
+        h = _new(stream, (M, F), torch.bfloat16, a_codes.device)
     _buffer(h, M * F * 2, "h", torch.bfloat16)
     if ws is None:
-        ws = _empty_u8(quant_workspace_bytes(1), a_codes.device)
+        ws = _empty_u8(quant_workspace_bytes(1), a_codes.device, stream)
     _buffer(ws, 0, "ws")
     _check(lib().nvfp4_gemm_prequant_swiglu(_p(a_codes), _p(a_sf), _p(g_a), M, K, _p(w.codes), _p(w.sf), F,
                                             _p(w.g_w), _p(h), _p(ws), _nbytes(ws), _stream(stream)),
@@ -478,10 +501,10 @@ def fp8_kv_calibrate(X: torch.Tensor, scale=None, ws=None, stream=None) -> torch
     _input_2d(X, "X")
     rows, cols = X.shape
     if scale is None:
-        scale = torch.empty(1, dtype=torch.float32, device=X.device)
+        scale = _new(stream, 1, torch.float32, X.device)
     _buffer(scale, 4, "scale", torch.float32)
     if ws is None:
-        ws = _empty_u8(quant_workspace_bytes(1), X.device)
+        ws = _empty_u8(quant_workspace_bytes(1), X.device, stream)
     _buffer(ws, 0, "ws")
     _check(lib().nvfp4_fp8_kv_calibrate(_p(X), rows, cols, X.stride(0), _p(scale), _p(ws), _nbytes(ws),
                                         _stream(stream)), "nvfp4_fp8_kv_calibrate")
@@ -496,7 +519,7 @@ def fp8_kv_quantize(X: torch.Tensor, scale: torch.Tensor, out=None, stream=None)
     rows, cols = X.shape
     _buffer(scale, 4, "scale", torch.float32)
     if out is None:
-        out = torch.empty((rows, cols), dtype=torch.uint8, device=X.device)
+        out = _new(stream, (rows, cols), torch.uint8, X.device)
     # out may be a strided view (leading dimension out.stride(0)); every byte
     # the kernel writes lies inside its [rows, cols] extent
     if out.dtype != torch.uint8 or out.dim() != 2 or out.stride(1) != 1 or out.shape[0] < rows or \
@@ -535,24 +558,6 @@ def _attention():
                            L.nvfp4_fp8_kv_attention_workspace_bytes)), False)
         _native = m
     return _native
-
-
-def _new(stream, shape, dtype, device):
-    """An output or scratch tensor for a call on `stream` (None: the current
-    one).  It belongs to the stream that writes it: memory of the current
-    stream may still be in use there by calls that another stream does not
-    wait for.  The current stream, on which the caller goes on, is made known
-    to the allocator."""
-    if stream is None or device.type != "cuda":
-        return torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(stream, torch.cuda.Stream) or stream.device != device:
-        raise ValueError(f"stream must be a torch.cuda.Stream of {device} (got {stream!r})")
-    current = torch.cuda.current_stream(device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    if current != stream:
-        t.record_stream(current)
-    return t
 
 
 def qk_norm_rope(q, k, positions, inv_freq=None, q_weight=None, k_weight=None, eps=1e-6, plus_one=False, q_out=None,
