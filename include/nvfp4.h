@@ -391,7 +391,8 @@ typedef struct {
  * key.  Lengths or offsets out of range, and table entries outside [0,
  * num_pages), latch NVFP4_ERR_INVALID_ARG (nvfp4_get_status); memory outside
  * the pages is never touched, the affected sequences' outputs are
- * unspecified. */
+ * unspecified.  max_pages * page_size is at most 2^31 - 256, num_seqs 2^20;
+ * beyond: NVFP4_ERR_UNSUPPORTED_SHAPE. */
 typedef struct {
     const int32_t *page_table;
     const int32_t *cu_tokens;
@@ -472,8 +473,11 @@ size_t nvfp4_fp8_kv_attention_workspace_bytes(int64_t tokens, int64_t q_heads, i
  * enter the FP8 MMA as the sum of two E4M3 terms, which hold all 8 bits of a
  * bf16 value (values below 2^-10 of their row's largest lose low bits),
  * probabilities as the sum of two E4M3 terms of 8 bits together; for single
- * tokens both are f16: queries exact, probabilities of 11 bits.  The order of the sums depends on the
+ * tokens both are f16: queries exact, probabilities of 11 bits.  These
+ * roundings are to nearest, ties to even.  The order of the sums depends on the
  * lengths of the whole batch: the same call gives the same bits.
+ * A scale that is not a positive finite number: no result is written and
+ * NVFP4_ERR_NONFINITE is latched.
  * ws: nvfp4_fp8_kv_attention_workspace_bytes(...) bytes, 16-byte aligned,
  * scratch only: nothing is kept in it between calls. */
 int nvfp4_fp8_kv_attention(const nvfp4_heads *q, const nvfp4_heads *gate, const nvfp4_heads *out, int64_t tokens,

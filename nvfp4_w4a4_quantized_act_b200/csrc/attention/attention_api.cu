@@ -308,22 +308,26 @@ attn::Parts parts_at(uint8_t *base, int64_t rows)
 // Where a batch may hold both kinds of sequences, the single tokens get their
 // own kernel beside the tile kernel from this many single items on (sequences
 // x key heads).  Measured (us, both kernels against the tile kernel alone):
-// 64 x 4 heads of 256, 8192 keys, one chunk of 512: 226 against 212; 16 x 4
-// with a chunk of 1000: 183 against 153; 200 x 4 with 2000 keys: 166 against
-// 187; 48 x 8 heads of 128, 4000 keys: 127 against 141; 128 x 8: 128 against
-// 169; 32 x 8: 60 against 59.
+// 64 x 4 heads of 256, 8192 keys, a chunk of 512: 201 against 203; 16 x 4, 4000
+// keys, a chunk of 1000: 144 against 121; 200 x 4, 2000 keys, 512: 138 against
+// 189; 8 heads of 128, 4000 keys, a chunk of 500: 32 x 8: 104 against 107; 48 x
+// 8: 120 against 131; 128 x 8: 192 against 235.
 constexpr int32_t kMixedItems = 370;
 // Rows beyond the sequences up to which a batch counts as padded single
-// tokens.  For single tokens alone (us, their kernel against the tile
-// kernel): 64 x 8192 keys of 4 heads of 256: 101 against 122; 64 x 500: 27
-// against 44; 1 x 777: 15.3 against 16.7; 256 x 1000 keys of 8 heads of 128:
-// 86 against 171.
+// tokens.  For padded single tokens alone (us, both kernels against the tile
+// kernel alone): 64 x 8192 keys of 4 heads of 256: 98 against 123; 64 x 500: 25
+// against 44; 1 x 777: 13.4 against 16.3; 256 x 1000 keys of 8 heads of 128: 85
+// against 184.
 constexpr int32_t kPadRows = 8;
 // What an item costs beside its keys, in keys: the time from one item's last
 // block to the next one's first.  Tile kernel, D = 256: 20 thousand cycles (a
-// block of 128 keys: 2300 to 2600); a prompt of 8192 takes 866 us at 512 and
-// 815 at 1152.  Single tokens, D = 256: 64 x 8192 takes 107 us at 32, 105 at
-// 128, 101 at 320; D = 128: 256 x 1000 takes 101 at 32, 86 at 128, 93 at 320.
+// block of 128 keys: 2300 to 2600); a prompt of 8192 takes 1010 us at 512, 917
+// at 768, 800 to 850 at 1152.  D = 128 (32 heads on 8), at 256, 384, 512, 768
+// and 1024: a prompt of 4000 takes 271, 244, 223, 219 and 226 us, four chunks of
+// 509 with up to 16384 keys 329, 320, 312, 304 and 307, 1000 tokens beside 23
+// single ones 145, 137, 136, 137 and 139.  Single tokens, D = 256: 64 x 8192
+// takes 105 us at 32, 102 at 128, 99 at 320; D = 128: 256 x 1000 takes 101 at
+// 32, 85 at 128, 92 at 320.
 constexpr int32_t kTileItemCost256 = 1152, kTileItemCost128 = 512, kDecodeItemCost256 = 320, kDecodeItemCost128 = 128;
 
 // Heads that one warp of the row kernels takes, sharing the token's angles:

@@ -12,9 +12,10 @@
 // little was in flight (8192 tokens x 28 heads of 256: 54 us, now 45, 5.3 TB/s
 // of 6.45; append of 8192 tokens x 4 heads: 16.4, now 15.1, 3.3 TB/s, where
 // the IEEE division and the conversions of 8 elements a lane count too).  A
-// row of 256 (128) elements is held by 32 (16) lanes, 8 elements each.  The lanes of the rotated part hold 4 elements of the first
-// half and their 4 partners of the second, so a pair turns inside a lane; the
-// others hold 8 neighbours.  The angle is the expensive part (an fp64 product
+// row of 256 (128) elements is held by 32 (16) lanes, 8 elements each.  The
+// lanes of the rotated part hold 4 elements of the first half and their 4
+// partners of the second, so a pair turns inside a lane; the others hold 8
+// neighbours.  The angle is the expensive part (an fp64 product
 // and reduction, a sine and cosine) and the same for every head: the warp
 // computes its token's angles once, a lane each, while the rows are on their
 // way.

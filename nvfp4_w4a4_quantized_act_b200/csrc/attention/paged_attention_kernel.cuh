@@ -16,10 +16,10 @@
 //   largest, off by at most 2^-17 of the largest below.
 //   Probabilities: 2^(t - r + 8), in f16; high keeps 4 significant bits by
 //   truncation, low = E4M3(p - high), ties to even: 8 bits together, as bf16
-//   would keep, but no finer than 2^-9.  So the reference r has to keep the probabilities up:
-//   it follows the blocks of 128 keys both ways, not only up as a running
-//   maximum would (after a key far above the rest, a sink, the others would
-//   lose their bits).  r moves up when a block's largest t is more than 0.75
+//   would keep, but no finer than 2^-9.  So the reference r has to keep the
+//   probabilities up: it follows the blocks of 128 keys both ways, not only up
+//   as a running maximum would (after a key far above the rest, a sink, the
+//   others would lose their bits).  r moves up when a block's largest t is more than 0.75
 //   above it (2^8.75 < 448), and down when it is more than 3 below while the
 //   sum so far is under 32 for each block: so the 128 errors of at most 2^-9
 //   of a block stay under 2^-7 of its share of the sum, in the worst case of
@@ -49,10 +49,13 @@
 // maximum, 300 for the reference, 2 x 800 for powers and terms), and powers
 // moved from the special-function unit to the FMA pipe made it slower.
 //
-// Measured (24 query heads on 4 key heads of 256): four chunks of 509 tokens
-// over histories to 16384, 354 GFLOP, 312 us, 1.13 PFLOP/s; a prompt of 8192,
-// 825 GFLOP, 815 us, 1.01 PFLOP/s, where the board's 1.63 for plain 16-bit
-// products is the measure.  A block takes 2300 to 2600 cycles, 2130 of them
+// Measured, the same call again and again (24 query heads on 4 key heads of
+// 256): four chunks of 509 tokens over histories to 16384, 354 GFLOP, 314 us,
+// 1.13 PFLOP/s; a prompt of 8192, 825 GFLOP, 800 to 850 us, 0.97 to 1.03
+// PFLOP/s, where the board's 1.63 for plain 16-bit products is the measure
+// (among other calls, with inputs that change, 362 and 858 us).  32 heads on 8
+// of 128: a prompt of 4000, 131 GFLOP, 223 us, 0.59 PFLOP/s: the softmax is the
+// same for half the products.  At D = 256 a block takes 2300 to 2600 cycles, 2130 of them
 // on the tensor cores: the softmax bounds it.  From one item's last block to
 // the next one's first go 20 thousand cycles (8 rows of queries a warp split
 // into terms, and a row of results a lane, gated): at D = 256 the accumulator
@@ -481,8 +484,8 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
         }
     } else if (warp == 1) {
         // ------------------------------------------------------ MMAs
-        // One lane, elected: with the election the compiler keeps descriptors and loop state in uniform registers, and
-        // an MMA takes 10 instructions instead of 24.  This thread's own instructions are what bounds the MMA rate.
+        // One lane, elected: with `lane == 0` in place of the election a prompt of 8192 takes 910 us instead of 800 to
+        // 850 and chunks of 509 take 378 instead of 340.
         if (elect_one()) {
             // E4M3 x E4M3 -> fp32, M = 128; scores: N = 128 keys, K-major; values: N = D, V's dimensions contiguous
             constexpr uint32_t IDESC_S = (1u << 4) | (uint32_t(KEY_BLOCK >> 3) << 17) | (uint32_t(ROW_TILE >> 4) << 24);

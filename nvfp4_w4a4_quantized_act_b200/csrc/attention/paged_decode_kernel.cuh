@@ -33,11 +33,11 @@
 // odd n, which makes both reads free of bank conflicts under the swizzle.
 //
 // Measured (24 query heads on 4 key heads of 256, parts joined): 64 sequences
-// of up to 8192 keys, 527 MB, 101 us, 5.2 TB/s; 2 of 131072, 537 MB, 99 us,
-// 5.4 TB/s (a copy on this board runs at 6.45).  A CTA's start (offsets, page
-// table, first keys: three loads that wait for one another), the join and the
-// launches take some 13 us of each; one sequence of 777 keys takes 15 us for
-// them alone.
+// of up to 8192 keys, 527 MB, 99 us, 5.3 TB/s; 2 of 131072, 537 MB, 96 us, 5.6
+// TB/s (a copy on this board runs at 6.45).  A CTA's start (offsets, page table,
+// first keys: three loads that wait for one another), the join and the launches
+// take some 13 us of each; one sequence of 777 keys takes 11 us for them alone,
+// 13.5 with an idle tile kernel beside it.
 #pragma once
 
 #include <climits>
