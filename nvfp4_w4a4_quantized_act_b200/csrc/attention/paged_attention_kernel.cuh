@@ -946,14 +946,20 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
                 named_barrier_sync(1 + quarter, 64);  // the two warps of these rows
                 if (warp_live) {
                     const float2 other = sm->red[buf][half ^ 1][row];
-                    const float tm = fmaxf(mine, other.x) * f;
-                    // ref is -inf until the row has seen a key; one branch for the warp, few blocks take it
-                    const bool up = tm > ref + REF_UP;
-                    const bool down = tm < ref - REF_DOWN && so_far + other.y < BLOCK_SUM / P_UNIT * static_cast<float>(j) && tm > -INFINITY;
+                    const float most = fmaxf(mine, other.x), tm = most * f;
+                    // How far the block's largest lies above the reference, rounded as its power's exponent is: from tm,
+                    // which is rounded before the difference, scores of millions would pass for smaller ones than they
+                    // are, and their power leave E4M3.  ref is -inf until the row has seen a key; one branch for the warp,
+                    // few blocks take it.
+                    const float above = fmaf(most, f, -ref);
+                    const bool up = above > REF_UP;
+                    const bool down = above < -REF_DOWN && so_far + other.y < BLOCK_SUM / P_UNIT * static_cast<float>(j) && tm > -INFINITY;
                     top = fmaxf(top, tm);
                     if (__any_sync(0xFFFFFFFFu, up || down)) {
                         if (up || down) {
-                            const float to = fmaxf(tm + (up ? SLACK_UP : SLACK_DOWN), top - REF_SPAN);
+                            float to = fmaxf(tm + (up ? SLACK_UP : SLACK_DOWN), top - REF_SPAN);
+                            if (fmaf(most, f, -to) > REF_UP)  // the steps of fp32 are wider than the slack
+                                to = fmaf(fabsf(tm), 0x1p-23f, to);
                             turn = ref > -INFINITY ? exp2_fast(ref - to) : 1.0f;
                             ref = to;
                             sum2 = mul2(sum2, pack2(turn, turn));

@@ -388,8 +388,9 @@ __global__ void __launch_bounds__(DECODE_THREADS, 1)
                     float turn[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
+                        // the difference is rounded as the powers' exponents are (paged_attention_kernel.cuh)
                         const float tm = mx[e] * f[e];
-                        const bool move = tm > -INFINITY && (!begun[e] || tm > ref[e] + P_ROOM);
+                        const bool move = tm > -INFINITY && (!begun[e] || fmaf(mx[e], f[e], -ref[e]) > P_ROOM);
                         turn[e] = move && begun[e] ? exp2_fast(ref[e] - tm) : 1.0f;
                         ref[e] = move ? tm : ref[e];
                         begun[e] = begun[e] || move;
