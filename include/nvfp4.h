@@ -475,7 +475,9 @@ size_t nvfp4_fp8_kv_attention_workspace_bytes(int64_t tokens, int64_t q_heads, i
  * probabilities as the sum of two E4M3 terms of 8 bits together; for single
  * tokens both are f16: queries exact, probabilities of 11 bits.  These
  * roundings are to nearest, ties to even.  The order of the sums depends on the
- * lengths of the whole batch: the same call gives the same bits.
+ * lengths of the whole batch: the same call gives the same bits.  Scores are
+ * fp32: beyond 2^25 in magnitude their steps are wider than the softmax's range
+ * and results are unspecified.
  * A scale that is not a positive finite number: no result is written and
  * NVFP4_ERR_NONFINITE is latched.
  * ws: nvfp4_fp8_kv_attention_workspace_bytes(...) bytes, 16-byte aligned,

@@ -1,5 +1,7 @@
 """Memory that the quantize, GEMM and FP8 cache calls allocate when they run on
 another stream than the current one, and their results there."""
+import types
+
 import pytest
 import torch
 
@@ -38,6 +40,19 @@ def _tensors(x):
     if isinstance(x, torch.Tensor):
         return [x]
     return [t for y in (x if isinstance(x, (tuple, list)) else [x.codes, x.sf, x.g_w]) for t in _tensors(y)]
+
+
+def test_a_stream_of_another_library():
+    """Whatever has the address of a CUDA stream serves as one."""
+    calls, side = _calls(), torch.cuda.Stream()
+    want = calls["linear_fused"]()
+    torch.cuda.synchronize()
+    got = calls["linear_fused"](stream=types.SimpleNamespace(cuda_stream=side.cuda_stream))
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    for bad in (7, "x", types.SimpleNamespace(cuda_stream="x")):
+        with pytest.raises(ValueError, match="stream"):
+            calls["linear_fused"](stream=bad)
 
 
 @pytest.mark.parametrize("name", sorted(["quantize_weights", "quantize_weights_gated", "quantize_act", "gemm_prequant", "linear_fused",
