@@ -412,6 +412,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
         return fail ? Item::none() : sm->items[i % ITEMS];
     };
 
+    uint32_t filled = 0, phases = 0;  // stages that this warp has filled, and the last time's phases
     if (warp == 0 || warp == 3) {
         // ------------------------------------------------------ loads
         // Warp 0 fetches the K blocks, warp 3 the V blocks, into the ring in the order K0 K1 V0 K2 V1 .. K(n-1) V(n-2)
@@ -425,7 +426,6 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
         const int row_at = is_k ? p.k_row_at : p.v_row_at, head_at = is_k ? p.k_head_at : p.v_head_at;
         uint32_t base = 0;  // ring stages of the items before
         bool fail = false, out_of_pool = false;
-        uint32_t filled = 0, phases = 0;  // stages that this warp has filled, and the last time's phases
         for (int i = 0;; ++i) {
             const Item it = warp_item(i, fail);
             if (it.blocks == 0)
@@ -475,13 +475,8 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
         }
         if (out_of_pool)
             atomicOr(p.status, kStatusBadIndex);
-        if (fail && lane == 0) {
+        if (fail && lane == 0)
             attn_timeout(sm, p.status);
-            // copies in flight land before the shared memory goes away
-            for (int f = 0; f < A::STAGES; ++f)
-                if (filled >> f & 1u)
-                    mbar_wait(smem_u32(&sm->full[f]), phases >> f & 1u, ATTN_DRAIN_NS);
-        }
     } else if (warp == 1) {
         // ------------------------------------------------------ MMAs
         // One lane, elected: with `lane == 0` in place of the election a prompt of 8192 takes 910 us instead of 800 to
@@ -1030,6 +1025,13 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1)
 
     tc_fence_before();
     __syncthreads();
+    // When some wait ran out, whosever it was, copies may be in flight that nobody has waited for: they land before
+    // the shared memory goes away.
+    if ((warp == 0 || warp == 3) && lane == 0 && sm->abort_flag) {
+        for (int f = 0; f < A::STAGES; ++f)
+            if (filled >> f & 1u)
+                mbar_wait(smem_u32(&sm->full[f]), phases >> f & 1u, ATTN_DRAIN_NS);
+    }
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();

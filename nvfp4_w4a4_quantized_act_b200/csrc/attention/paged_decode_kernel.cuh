@@ -174,6 +174,7 @@ __global__ void __launch_bounds__(DECODE_THREADS, 1)
             atomicOr(p.status, kStatusBadIndex);
     }
 
+    uint32_t fills = 0;  // of the loading warp: stages filled so far
     if (warp == DECODE_WARPS) {
         // ------------------------------------------------ items, loads
         Walk walk;
@@ -189,7 +190,6 @@ __global__ void __launch_bounds__(DECODE_THREADS, 1)
         const int shift = p.batch.page_shift, page = 1 << shift;
         const int rows = min(page, KEY_BLOCK);        // rows of a box
         const int boxes = KEY_BLOCK / rows;
-        uint32_t fills = 0;
         bool fail = false, out_of_pool = false;
         for (int i = 0;; ++i) {
             int64_t end_cost = 0;
@@ -270,12 +270,8 @@ __global__ void __launch_bounds__(DECODE_THREADS, 1)
         }
         if (out_of_pool)
             atomicOr(p.status, kStatusBadIndex);
-        if (fail && lane == 0) {
+        if (fail && lane == 0)
             decode_timeout(sm, p.status);
-            // copies in flight land before the shared memory goes away
-            for (uint32_t f = fills > A::STAGES ? fills - A::STAGES : 0; f < fills; ++f)
-                mbar_wait(smem_u32(&sm->full[f % A::STAGES]), (f / A::STAGES) & 1u, ATTN_WAIT_NS);
-        }
         if (lane == 0)
             p.parts.info[cta] = info;
     } else if (warp < DECODE_WARPS) {
@@ -574,6 +570,11 @@ __global__ void __launch_bounds__(DECODE_THREADS, 1)
         store_amax(p, amax, lane);
     }
     __syncthreads();
+    // when some wait ran out: copies in flight land before the shared memory goes away
+    if (warp == DECODE_WARPS && lane == 0 && sm->abort_flag) {
+        for (uint32_t f = fills > A::STAGES ? fills - A::STAGES : 0; f < fills; ++f)
+            mbar_wait(smem_u32(&sm->full[f % A::STAGES]), (f / A::STAGES) & 1u, ATTN_DRAIN_NS);
+    }
 }
 
 }  // namespace attn
